@@ -1,0 +1,540 @@
+"""The attention half of a decode step, operator by operator: what is computed, on which sizes.
+
+`listed()` names the measured cases, `draw()` gives more of the same ranges, `prepare()` makes the
+inputs, `run()` computes one pass (plain torch operations, or with `own` the library's kernels),
+`work()` counts the bytes and operations that cannot be avoided and `exact()` evaluates the
+definitions in 64 bits.
+
+Operators: q4_matvec (projections with 4-bit weights and group scales), block_tables (page tables
+and slot maps of a step), kv_append (new rows into the paged cache) and tree_attention (one or
+several drafted tokens per request over the cache).
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+DEV = "cuda"
+RMS_EPS = 1e-5
+
+
+# --------------------------------------------------------------------------- cases
+def _matvec(name, rows, cols, group, tokens, zeros=False, rms=False, bias=False, resid=False):
+    return dict(name=name, op="matvec", rows=rows, cols=cols, group=group, tokens=tokens,
+                zeros=zeros, rms=rms, bias=bias, resid=resid)
+
+
+def _tables(name, requests, context, new, page):
+    return dict(name=name, op="tables", requests=requests, context=context, new=new, page=page)
+
+
+def _append(name, tokens, kv_heads, dim, cache, page, src="f32"):
+    return dict(name=name, op="append", tokens=tokens, kv_heads=kv_heads, dim=dim, cache=cache,
+                page=page, src=src)
+
+
+def _attend(name, requests, context, new, heads, kv_heads, dim, cache, page, q="f32"):
+    return dict(name=name, op="attend", requests=requests, context=context, new=new, heads=heads,
+                kv_heads=kv_heads, dim=dim, cache=cache, page=page, q=q)
+
+
+def listed():
+    return [
+        # output projection of the 7B-shaped stack, one token, blocks of 32 as in Q4_0: latency
+        _matvec("matvec out 4096 b1", 4096, 4096, 32, 1, resid=True),
+        # fused query/key/value projection of the 70B-shaped stack (64 + 2*8 heads of 128)
+        _matvec("matvec qkv 70b b1", 10240, 8192, 128, 1, zeros=True, rms=True),
+        # the 40B-shaped stack's (128 + 2*8 heads of 64) for five drafted tokens
+        _matvec("matvec qkv 40b b5", 9216, 8192, 64, 5, zeros=True, rms=True),
+        # the 175B-shaped stack's, with biases, for a full batch: the largest product
+        _matvec("matvec qkv 175b b16", 36864, 12288, 64, 16, rms=True, bias=True),
+        # one new token for each of 16 requests: the step of a small server
+        _tables("tables decode r16", 16, 4096, 1, 16),
+        # a mixed step: 512 ragged requests, some of them with whole prompts
+        _tables("tables mixed r512", 512, 8192, 257, 64),
+        # the rows of one decode step of 16 tokens, cut from the fused projection
+        _append("append step 16", 16, 8, 128, "f16", 16),
+        # a prompt of odd length into 8-bit pages
+        _append("append prompt fp8", 8191, 8, 128, "fp8", 64),
+        # one token of one request, grouped heads: the shortest path of a chat
+        _attend("attend b1 gqa 4k", 1, 4096, 1, 64, 8, 128, "f16", 16),
+        # trees of up to 16 drafted tokens for four requests (70B-shaped heads)
+        _attend("attend tree16 gqa 8k", 4, 8193, 16, 64, 8, 128, "f16", 64),
+        # sixteen requests of one token each, a key head per query head (175B-shaped)
+        _attend("attend b16 mha 4k", 16, 4095, 1, 96, 96, 128, "f16", 16),
+        # trees of 64 over long 8-bit caches, 16 query heads to a key head (40B-shaped)
+        _attend("attend tree64 fp8 32k", 2, 32768, 64, 128, 8, 64, "fp8", 64, q="f16"),
+    ]
+
+
+def _log(rng, lo, hi):
+    """An integer in [lo, hi], spread over its logarithm."""
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["matvec", "tables", "append", "attend"])
+    if op == "matvec":
+        case = _matvec("", _log(rng, 256, 36864), 32 * _log(rng, 16, 384), rng.choice([32, 64, 128]),
+                       rng.randint(1, 16), rng.random() < 0.5, rng.random() < 0.5,
+                       rng.random() < 0.3, rng.random() < 0.5)
+    elif op == "tables":
+        case = _tables("", _log(rng, 1, 1024), _log(rng, 1, 16384), _log(rng, 1, 257),
+                       rng.choice([16, 32, 64, 128]))
+    elif op == "append":
+        case = _append("", _log(rng, 1, 8191), rng.choice([1, 2, 4, 8]), rng.choice([64, 96, 128]),
+                       rng.choice(["f16", "fp8"]), rng.choice([16, 32, 64, 128]),
+                       rng.choice(["f32", "f16"]))
+    else:
+        while True:
+            kv = rng.choice([1, 2, 4, 8, 32, 96])
+            group = rng.choice([1, 2, 3, 4, 5, 7, 8, 12, 16]) if kv <= 8 else 1
+            case = _attend("", _log(rng, 1, 32), _log(rng, 1, 65536), _log(rng, 1, 64), kv * group,
+                           kv, rng.choice([64, 96, 128, 256]), rng.choice(["f16", "fp8"]),
+                           rng.choice([16, 32, 64, 128]), rng.choice(["f32", "f16"]))
+            # no more keys, padded or not, and no more products than the largest listed cases
+            keys = case["requests"] * (case["context"] + case["new"]) * kv * case["dim"]
+            if keys <= 16 * 4096 * 96 * 128 and \
+                    keys * case["new"] * group <= 2 * 32832 * 64 * 128 * 64:
+                break
+    del case["name"]
+    return case
+
+
+# --------------------------------------------------------------------------- lengths of a case
+def _spread(i, top, lowest):
+    """The i-th of a ragged set of lengths in [lowest, top]; the first is the longest."""
+    return top if i == 0 else lowest + int((top - lowest) * ((i * 0.6180339887) % 1.0))
+
+
+def _lengths(case):
+    """Tokens in the cache and tokens of this step, per request (the case alone fixes them)."""
+    n = case["requests"]
+    lens = [_spread(i, case["context"], 0) for i in range(n)]
+    if case["op"] == "tables":
+        # every eighth request brings many tokens, the others one
+        adds = [_spread(i // 8, case["new"], 1) if i % 8 == 0 else 1 for i in range(n)]
+    else:
+        adds = [_spread(n - 1 - i, case["new"], 1) for i in range(n)]
+    return lens, adds
+
+
+def _pages(tokens, page):
+    return -(-tokens // page)
+
+
+def _i32(values):
+    return torch.tensor(values, dtype=torch.int32, device=DEV)
+
+
+# --------------------------------------------------------------------------- inputs
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(int(seed))
+
+
+def _activations(g, tokens, cols):
+    """Residual-stream rows: normal, with a few channels thirty times as large."""
+    x = torch.randn(tokens, cols, device=DEV, generator=g)
+    x[:, :: max(1, cols // 7)] *= 30.0
+    return x
+
+
+def _prepare_matvec(case, seed):
+    g = _gen(seed)
+    rows, cols, tokens = case["rows"], case["cols"], case["tokens"]
+    groups = _pages(cols, case["group"])
+    s = dict(case=case)
+    s["codes"] = torch.randint(0, 256, (rows, cols // 2), dtype=torch.uint8, device=DEV,
+                               generator=g)
+    s["scales"] = (torch.rand(rows, groups, device=DEV, generator=g) * 0.004 + 0.001).half()
+    s["zeros"] = torch.randint(4, 12, (rows, groups), dtype=torch.uint8, device=DEV,
+                               generator=g) if case["zeros"] else None
+    s["x"] = _activations(g, tokens, cols)
+    s["bias"] = torch.randn(rows, device=DEV, generator=g) if case["bias"] else None
+    s["resid"] = torch.randn(tokens, rows, device=DEV, generator=g) if case["resid"] else None
+    s["y"] = torch.empty(tokens, rows, device=DEV)
+    if own:
+        import activation_sparse_mlp_amd as spffn
+        s["w"] = spffn.Q4Matrix(s["codes"], s["scales"], s["zeros"], group=case["group"])
+    return s
+
+
+def _prepare_tables(case, seed):
+    rnd = random.Random(seed)
+    page, n = case["page"], case["requests"]
+    lens, adds = _lengths(case)
+    width = _pages(case["context"] + case["new"], page) + 1
+    held = [_pages(t, page) for t in lens]
+    need = [_pages(t + a, page) - h for t, a, h in zip(lens, adds, held)]
+    ids = list(range(sum(held) + sum(need) + 5))
+    rnd.shuffle(ids)
+    table = torch.full((n, width), -1, dtype=torch.int32)
+    at = 0
+    for r in range(n):
+        table[r, :held[r]] = torch.tensor(ids[at:at + held[r]], dtype=torch.int32)
+        at += held[r]
+    tokens = sum(adds) + 3  # the buffers of a step are a little longer than its tokens
+    free = ids[at:]
+    return dict(case=case, lens=_i32(lens), adds=_i32(adds), table=table.to(DEV),
+                free=_i32(free), n_free=_i32([len(free)]), tokens=tokens,
+                starts=torch.empty(n + 1, dtype=torch.int32, device=DEV),
+                new_lens=torch.empty(n, dtype=torch.int32, device=DEV),
+                slots=torch.empty(tokens, dtype=torch.int32, device=DEV),
+                positions=torch.empty(tokens, dtype=torch.int32, device=DEV),
+                left=torch.empty(2, dtype=torch.int32, device=DEV))
+
+
+_CACHE = {"f16": torch.float16, "fp8": torch.float8_e4m3fn}
+_SRC = {"f32": torch.float32, "f16": torch.float16}
+
+
+def _packet(cache):
+    """Elements of a 16-byte packet, the unit of the cache's layout."""
+    return 8 if cache == "f16" else 16
+
+
+def _empty_cache(g, case, pages):
+    """Pages [pages, heads, dim/E, page, E] of keys and [pages, heads, page/E, dim, E] of values,
+    filled with earlier tokens, and for 8-bit pages a scale per head."""
+    e, h, d, p = _packet(case["cache"]), case["kv_heads"], case["dim"], case["page"]
+    k = torch.randn(pages, h, d // e, p, e, device=DEV, generator=g)
+    k[:, :, 0, :, 0] *= 4.0  # keys have a channel that stands out
+    v = torch.randn(pages, h, p // e, d, e, device=DEV, generator=g)
+    if case["cache"] == "f16":
+        return k.half(), v.half(), None, None
+    ks = torch.rand(h, device=DEV, generator=g) * 0.02 + 0.02
+    vs = torch.rand(h, device=DEV, generator=g) * 0.02 + 0.01
+    k = (k / ks.view(1, h, 1, 1, 1)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    v = (v / vs.view(1, h, 1, 1, 1)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    return k, v, ks, vs
+
+
+def _handle(s):
+    if own:
+        import activation_sparse_mlp_amd as spffn
+        s["cache"] = spffn.KVCache(s["k"], s["v"], s["k_scale"], s["v_scale"])
+
+
+def _prepare_append(case, seed):
+    g = _gen(seed)
+    n, h, d, p = case["tokens"], case["kv_heads"], case["dim"], case["page"]
+    pages = _pages(n, p) + 2
+    s = dict(case=case)
+    s["k"], s["v"], s["k_scale"], s["v_scale"] = _empty_cache(g, case, pages)
+    # the new rows are parts of the rows that the fused projection wrote (as many query heads)
+    qkv = torch.randn(n, 3 * h, d, device=DEV, generator=g).to(_SRC[case["src"]])
+    s["new_k"], s["new_v"] = qkv[:, h:2 * h], qkv[:, 2 * h:]
+    order = torch.randperm(pages, device=DEV, generator=g)
+    at = torch.arange(n, device=DEV) + p // 2  # the first page is half full already
+    s["slots"] = (order[at // p] * p + at % p).to(torch.int32)
+    if n > 4:
+        s["slots"][n // 2] = -1  # a padded token writes nothing
+    _handle(s)
+    return s
+
+
+def _tree(rnd, n):
+    """Ancestor bits (itself included) of the n tokens of a random tree, in drafting order."""
+    bits = []
+    for i in range(n):
+        parent = rnd.randint(max(-1, i - 4), i - 1)
+        bits.append((bits[parent] if parent >= 0 else 0) | 1 << i)
+    return [b - (1 << 64) if b >> 63 else b for b in bits]
+
+
+def _prepare_attend(case, seed):
+    g, rnd = _gen(seed), random.Random(seed)
+    p, d = case["page"], case["dim"]
+    lens, adds = _lengths(case)
+    held = [_pages(t + a, p) for t, a in zip(lens, adds)]
+    width = max(held)
+    ids = list(range(sum(held) + 1))
+    rnd.shuffle(ids)
+    table = torch.full((len(lens), width), -1, dtype=torch.int32)
+    at = 0
+    for r in range(len(lens)):
+        table[r, :held[r]] = torch.tensor(ids[at:at + held[r]], dtype=torch.int32)
+        at += held[r]
+    s = dict(case=case, lens=_i32(lens), table=table.to(DEV), max_new=max(adds))
+    s["k"], s["v"], s["k_scale"], s["v_scale"] = _empty_cache(g, case, len(ids))
+    starts = [0]
+    for a in adds:
+        starts.append(starts[-1] + a)
+    s["starts"] = _i32(starts)
+    s["mask"] = torch.tensor([b for a in adds for b in _tree(rnd, a)], dtype=torch.int64,
+                             device=DEV)
+    s["q"] = torch.randn(starts[-1], case["heads"], d, device=DEV, generator=g).to(
+        _SRC[case["q"]])
+    s["scale"] = d ** -0.5
+    s["out"] = torch.empty_like(s["q"])
+    _handle(s)
+    if own:
+        s["ws"] = s["cache"].workspace(case["heads"], s["max_new"])
+    return s
+
+
+def prepare(case, seed):
+    return {"matvec": _prepare_matvec, "tables": _prepare_tables, "append": _prepare_append,
+            "attend": _prepare_attend}[case["op"]](case, seed)
+
+
+# --------------------------------------------------------------------------- plain forms
+def _weights(codes, scales, zeros, group, cols, dtype):
+    q = torch.stack([codes & 15, codes >> 4], dim=-1).view(codes.shape[0], cols).to(dtype)
+    z = torch.full_like(scales, 8.0, dtype=dtype) if zeros is None else zeros.to(dtype)
+    at = torch.arange(cols, device=codes.device) // group
+    return (q - z[:, at]) * scales.to(dtype)[:, at]
+
+
+def _plain_matvec(s):
+    case, x = s["case"], s["x"]
+    if case["rms"]:
+        x = x / torch.sqrt((x * x).mean(dim=1, keepdim=True) + RMS_EPS)
+    w = _weights(s["codes"], s["scales"], s["zeros"], case["group"], case["cols"], torch.float32)
+    y = x @ w.t()
+    if s["bias"] is not None:
+        y = y + s["bias"]
+    if s["resid"] is not None:
+        y = y + s["resid"]
+    return y
+
+
+def _plain_tables(s):
+    page, table, free = s["case"]["page"], s["table"], s["free"].long()
+    lens, adds, n_free = s["lens"].long(), s["adds"].long(), s["n_free"].long()
+    n, width = table.shape
+    held = (lens + page - 1) // page
+    fits = lens + adds <= width * page
+    need = torch.where(fits, (lens + adds + page - 1) // page - held, 0)
+    upto = need.cumsum(0)
+    off = upto - need
+    served = fits & (upto <= n_free)
+    # table entries of the new pages
+    col = torch.arange(width, device=DEV).view(1, -1)
+    fresh = (col >= held[:, None]) & (col < (held + need)[:, None]) & served[:, None]
+    pick = n_free - 1 - (off[:, None] + col - held[:, None])
+    filled = torch.where(fresh, free[pick.clamp(0, free.numel() - 1)], table.long())
+    table.copy_(filled)
+    # tokens
+    ends = adds.cumsum(0)
+    token = torch.arange(s["tokens"], device=DEV)
+    r = torch.searchsorted(ends, token, right=True).clamp(max=n - 1)
+    at = lens[r] + token - (ends - adds)[r]
+    real = token < ends[-1]
+    entry = filled[r, (at // page).clamp(0, width - 1)]
+    slots = torch.where(real & served[r] & (entry >= 0), entry * page + at % page, -1)
+    starts = torch.cat([ends.new_zeros(1), ends])
+    left = torch.stack([n_free[0] - torch.where(served, need, 0).sum(), (~served).sum()])
+    return dict(table=table, starts=starts.int(), slots=slots.int(),
+                positions=torch.where(real, at, -1).int(),
+                new_lens=torch.where(served, lens + adds, lens).int(), left=left.int())
+
+
+def _plain_append(s):
+    case, k, v = s["case"], s["k"], s["v"]
+    e, p, d, h = _packet(case["cache"]), case["page"], case["dim"], case["kv_heads"]
+    new_k, new_v = s["new_k"].float(), s["new_v"].float()
+    if s["k_scale"] is not None:
+        new_k = (new_k / s["k_scale"].view(1, h, 1)).clamp(-448, 448)
+        new_v = (new_v / s["v_scale"].view(1, h, 1)).clamp(-448, 448)
+    raw = torch.int16 if case["cache"] == "f16" else torch.uint8
+    new_k, new_v = new_k.to(k.dtype).view(raw), new_v.to(v.dtype).view(raw)
+    slots = s["slots"].long()
+    # a padded token goes to a page behind the last one, which is dropped again
+    page = torch.where(slots >= 0, slots // p, k.shape[0])
+    at = torch.where(slots >= 0, slots % p, 0)
+    more = lambda t: torch.cat([t.view(raw), t[:1].view(raw)])  # noqa: E731
+    big_k, big_v = more(k), more(v)
+    big_k[page, :, :, at] = new_k.view(-1, h, d // e, e)
+    big_v[page, :, at // e, :, at % e] = new_v
+    k.view(raw).copy_(big_k[:-1])
+    v.view(raw).copy_(big_v[:-1])
+    return k, v
+
+
+def _plain_attend(s):
+    case, k, v = s["case"], s["k"], s["v"]
+    h, d, p, t = case["kv_heads"], case["dim"], case["page"], s["max_new"]
+    group = case["heads"] // h
+    n, width = s["table"].shape
+    pages = s["table"].long().clamp(min=0)
+    keys = k[pages].float().permute(0, 2, 1, 4, 3, 5).reshape(n, h, width * p, d)
+    values = v[pages].float().permute(0, 2, 1, 3, 5, 4).reshape(n, h, width * p, d)
+    starts, lens = s["starts"].long(), s["lens"].long()
+    adds = starts[1:] - starts[:-1]
+    token = torch.arange(s["q"].shape[0], device=DEV)
+    r = torch.searchsorted(starts[1:], token, right=True)
+    at = token - starts[r]
+    every = (starts[:-1, None] + torch.arange(t, device=DEV)).clamp(max=token.numel() - 1)
+    q = s["q"].float()[every].view(n, t, h, group, d).permute(0, 2, 1, 3, 4)
+    scores = q.reshape(n, h, t * group, d) @ keys.transpose(2, 3).contiguous() * s["scale"]
+    if s["k_scale"] is not None:
+        scores = scores * s["k_scale"].view(1, h, 1, 1)
+    j = torch.arange(width * p, device=DEV).view(1, 1, -1) - lens.view(n, 1, 1)
+    bit = (s["mask"][every][:, :, None] >> j.clamp(0, 63)) & 1
+    seen = (j < 0) | ((j < adds.view(n, 1, 1)) & (bit == 1))
+    scores = scores.view(n, h, t, group, -1).masked_fill(~seen[:, None, :, None], -math.inf)
+    top = scores.amax(-1, keepdim=True)
+    weights = torch.exp(scores - top.masked_fill(top == -math.inf, 0.0))
+    total = weights.sum(-1, keepdim=True)
+    weights = weights / total.masked_fill(total == 0, 1.0)
+    o = weights.view(n, h, t * group, -1) @ values
+    if s["v_scale"] is not None:
+        o = o * s["v_scale"].view(1, h, 1, 1)
+    o = o.view(n, h, t, group, d).permute(0, 2, 1, 3, 4).reshape(n, t, h * group, d)
+    return o[r, at].to(s["q"].dtype)
+
+
+# --------------------------------------------------------------------------- a pass
+def run(s):
+    op = s["case"]["op"]
+    if not own:
+        return {"matvec": _plain_matvec, "tables": _plain_tables, "append": _plain_append,
+                "attend": _plain_attend}[op](s)
+    import activation_sparse_mlp_amd as spffn
+    if op == "matvec":
+        return spffn.q4_matvec(s["w"], s["x"], bias=s["bias"], resid=s["resid"],
+                               rms_eps=RMS_EPS if s["case"]["rms"] else None, y=s["y"])
+    if op == "tables":
+        out = spffn.block_tables(s["lens"], s["adds"], s["table"], s["free"], s["n_free"],
+                                 s["case"]["page"], s["tokens"], starts=s["starts"],
+                                 new_lens=s["new_lens"], slots=s["slots"],
+                                 positions=s["positions"], left=s["left"])
+        return dict(out, table=s["table"])
+    if op == "append":
+        spffn.kv_append(s["cache"], s["new_k"], s["new_v"], s["slots"])
+        return s["k"], s["v"]
+    return spffn.tree_attention(s["cache"], s["q"], s["starts"], s["lens"], s["table"],
+                                mask=s["mask"], scale=s["scale"], max_new=s["max_new"],
+                                out=s["out"], ws=s["ws"])
+
+
+# --------------------------------------------------------------------------- what it cannot avoid
+def work(case):
+    op = case["op"]
+    if op == "matvec":
+        rows, cols, t = case["rows"], case["cols"], case["tokens"]
+        groups = _pages(cols, case["group"])
+        b = rows * cols // 2 + rows * groups * (3 if case["zeros"] else 2)
+        b += 4 * t * (cols + rows * (2 if case["resid"] else 1)) + (4 * rows if case["bias"] else 0)
+        return dict(bytes=b, flops=2 * t * rows * cols)
+    if op == "append":
+        e = 2 if case["cache"] == "f16" else 1
+        src = 4 if case["src"] == "f32" else 2
+        n = case["tokens"]
+        return dict(bytes=n * 2 * case["kv_heads"] * case["dim"] * (src + e) + 4 * n, flops=0)
+    lens, adds = _lengths(case)
+    if op == "tables":
+        n, tokens, page = len(lens), sum(adds), case["page"]
+        new = sum(_pages(t + a, page) - _pages(t, page) for t, a in zip(lens, adds))
+        # lengths, counts, starts and new lengths; a free page and its entry; an entry of the
+        # table for each page that is written to; a slot and a position for each token
+        part = sum(1 for t, a in zip(lens, adds) if a and t % page)
+        return dict(bytes=16 * n + 8 * new + 4 * part + 8 * (tokens + 3), flops=0)
+    e = 2 if case["cache"] == "f16" else 1
+    qe = 4 if case["q"] == "f32" else 2
+    keys = sum(t + a for t, a in zip(lens, adds))
+    b = keys * case["kv_heads"] * case["dim"] * 2 * e
+    b += sum(adds) * (case["heads"] * case["dim"] * 2 * qe + 8)
+    b += 4 * sum(_pages(t + a, case["page"]) for t, a in zip(lens, adds))
+    flops = sum((t + a) * a for t, a in zip(lens, adds)) * case["heads"] * case["dim"] * 4
+    return dict(bytes=b, flops=flops)
+
+
+# --------------------------------------------------------------------------- definitions, 64 bits
+def _exact_matvec(s):
+    case, x = s["case"], s["x"].double()
+    y = torch.zeros(case["tokens"], case["rows"], dtype=torch.float64, device=DEV)
+    for c0 in range(0, case["cols"], case["group"]):  # y = sum over groups of s (q - z) . x
+        g, c1 = c0 // case["group"], min(c0 + case["group"], case["cols"])
+        part = s["codes"][:, c0 // 2:c1 // 2].to(torch.int32)
+        even, odd = (part % 16).double(), (part // 16).double()
+        z = 8.0 if s["zeros"] is None else s["zeros"][:, g:g + 1].double()
+        dot = x[:, c0:c1:2] @ (even - z).t() + x[:, c0 + 1:c1:2] @ (odd - z).t()
+        y += dot * s["scales"][:, g].double()
+    if case["rms"]:
+        y /= ((x ** 2).sum(1, keepdim=True) / case["cols"] + RMS_EPS) ** 0.5
+    if s["bias"] is not None:
+        y += s["bias"].double()
+    if s["resid"] is not None:
+        y += s["resid"].double()
+    return y
+
+
+def _exact_tables(s):
+    page = s["case"]["page"]
+    table, free = s["table"].cpu().clone(), s["free"].tolist()
+    lens, adds, have = s["lens"].tolist(), s["adds"].tolist(), int(s["n_free"])
+    n_free, short, asked = have, 0, 0
+    starts, slots, positions, new_lens = [0], [], [], []
+    for r, (t, a) in enumerate(zip(lens, adds)):
+        held, upto = -(-t // page), -(-(t + a) // page)
+        fits = upto <= table.shape[1]
+        asked += upto - held if fits else 0
+        ok = fits and asked <= n_free
+        if ok:
+            for b in range(held, upto):
+                table[r, b] = free[have - 1]
+                have -= 1
+        for i in range(t, t + a):
+            e = int(table[r, i // page]) if ok else -1
+            slots.append(e * page + i % page if e >= 0 else -1)
+            positions.append(i)
+        starts.append(starts[-1] + a)
+        new_lens.append(t + a if ok else t)
+        short += not ok
+    pad = [-1] * (s["tokens"] - len(slots))
+    as_int = lambda v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    return dict(table=table, starts=as_int(starts), slots=as_int(slots + pad),
+                positions=as_int(positions + pad), new_lens=as_int(new_lens),
+                left=as_int([have, short]))
+
+
+def _exact_append(s):
+    case, p, e = s["case"], s["case"]["page"], _packet(s["case"]["cache"])
+    h, d = case["kv_heads"], case["dim"]
+    k = s["k"].double().permute(0, 3, 1, 2, 4).reshape(-1, h, d)     # a row per slot
+    v = s["v"].double().permute(0, 2, 4, 1, 3).reshape(-1, h, d)
+    slots = s["slots"].long()
+    kept = slots >= 0
+    for to, new, scale in ((k, s["new_k"], s["k_scale"]), (v, s["new_v"], s["v_scale"])):
+        rows = new.double()
+        if scale is not None:
+            rows = (rows / scale.double()[:, None]).clamp(-448, 448)
+        to[slots[kept]] = rows[kept]
+    return (k.view(-1, p, h, d // e, e).permute(0, 2, 3, 1, 4).contiguous(),
+            v.view(-1, p // e, e, h, d).permute(0, 3, 1, 4, 2).contiguous())
+
+
+def _exact_attend(s):
+    case, p = s["case"], s["case"]["page"]
+    h, d = case["kv_heads"], case["dim"]
+    group = case["heads"] // h
+    starts, lens, mask = s["starts"].tolist(), s["lens"].tolist(), s["mask"].tolist()
+    out = torch.zeros(s["q"].shape, dtype=torch.float64, device=DEV)
+    for r, n in enumerate(lens):
+        a, b = starts[r], starts[r + 1]
+        total = n + b - a
+        pages = s["table"][r, :-(-total // p)].long()
+        k = s["k"][pages].double().permute(0, 3, 1, 2, 4).reshape(-1, h, d)[:total]
+        v = s["v"][pages].double().permute(0, 2, 4, 1, 3).reshape(-1, h, d)[:total]
+        if s["k_scale"] is not None:
+            k, v = k * s["k_scale"].double()[:, None], v * s["v_scale"].double()[:, None]
+        seen = torch.ones(b - a, total, dtype=torch.bool)
+        for i in range(b - a):
+            for j in range(b - a):
+                seen[i, n + j] = bool(mask[a + i] >> j & 1)
+        seen = seen.to(DEV)
+        for head in range(case["heads"]):
+            x = s["q"][a:b, head].double() @ k[:, head // group].t() * s["scale"]
+            x = torch.softmax(x.masked_fill(~seen, -math.inf), dim=1)
+            out[a:b, head] = torch.nan_to_num(x, nan=0.0) @ v[:, head // group]
+    return out
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return {"matvec": _exact_matvec, "tables": _exact_tables, "append": _exact_append,
+            "attend": _exact_attend}[case["op"]](s)
