@@ -310,7 +310,7 @@ def _plain_tables(s):
     need = torch.where(fits, (lens + adds + page - 1) // page - held, 0)
     upto = need.cumsum(0)
     off = upto - need
-    served = fits & (upto <= n_free)
+    served = fits & ((need == 0) | (upto <= n_free))  # no page wanted: nothing to wait for
     # table entries of the new pages
     col = torch.arange(width, device=DEV).view(1, -1)
     fresh = (col >= held[:, None]) & (col < (held + need)[:, None]) & served[:, None]
@@ -473,7 +473,7 @@ def _exact_tables(s):
         held, upto = -(-t // page), -(-(t + a) // page)
         fits = upto <= table.shape[1]
         asked += upto - held if fits else 0
-        ok = fits and asked <= n_free
+        ok = fits and (upto == held or asked <= n_free)
         if ok:
             for b in range(held, upto):
                 table[r, b] = free[have - 1]
