@@ -38,6 +38,17 @@ class LayerDesc(C.Structure):
                 ("p_w2", C.c_void_p), ("p_b2", C.c_void_p)]
 
 
+class Q4Desc(C.Structure):
+    _fields_ = [("packed", C.c_void_p), ("rows", C.c_int32), ("cols", C.c_int32),
+                ("group", C.c_int32), ("zeros", C.c_int32)]
+
+
+class CacheDesc(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("pages", C.c_int32), ("page_size", C.c_int32),
+                ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("dtype", C.c_int32)]
+
+
 class Trace(C.Structure):
     _fields_ = [("h_in", C.c_void_p), ("union_mask", C.c_void_p), ("logits", C.c_void_p),
                 ("events", C.c_void_p)]
@@ -74,6 +85,15 @@ SIGNATURES = {
     "spffn_hot_first_order": (_i32, [_vp, _i32, _vp, _vp]),
     "spffn_permute_rows": (_i32, [_vp, _vp, _vp, _i32, _i64, _vp]),
     "spffn_q4_0_repack": (_i32, [_vp, _vp, _i32, _i32, _vp]),
+    "spffn_q4_packed_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "spffn_q4_pack": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]),
+    "spffn_q4_matvec": (_i32, [_vp, _vp, _i32, _f32, _vp, _vp, _vp, _vp]),
+    "spffn_block_tables": (_i32, [_vp, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp,
+                                  _vp, _i32, _vp, _vp]),
+    "spffn_kv_append": (_i32, [_vp, _vp, _vp, _i32, _i64, _i64, _vp, _i32, _vp]),
+    "spffn_tree_attention_workspace_bytes": (_sz, [_vp, _i32, _i32, _i32]),
+    "spffn_tree_attention": (_i32, [_vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp, _i32, _i32,
+                                    _vp, _i32, _f32, _vp, _i64, _vp, _sz, _vp]),
     "spffn_stream_read": (_i32, [_vp, _i64, _vp, _vp]),
     "spffn_set_wait_limit": (_i32, [_i32]),
     "spffn_last_error": (C.c_char_p, []),
@@ -575,6 +595,273 @@ def q4_0_repack(aos, rows, cols, soa=None):
     _check(load().spffn_q4_0_repack(_ptr(aos), _ptr(soa), rows, cols, _stream()),
            "spffn_q4_0_repack")
     return soa
+
+
+# --------------------------------------------------------------------------- #
+# the attention half of a decode step
+# --------------------------------------------------------------------------- #
+MAX_REQUESTS = 4096
+MAX_NEW = 64
+_ROW_DTYPES = {torch.float32: F32, torch.float16: F16}
+_CACHE_DTYPES = {torch.float16: F16, torch.float8_e4m3fn: FP8_E4M3}
+
+
+def _call(dev, name, *args):
+    """One entry point on the current stream of the tensors' device, which need
+    not be the current device."""
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if status != 0:
+        _check(status, name)
+
+
+def _on(dev, **tensors):
+    """Raise ValueError unless every given tensor is on device dev."""
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+class Q4Matrix:
+    """A 4-bit matrix [rows, cols] with group scales, laid out for q4_matvec.
+
+    codes uint8 [rows, cols / 2] (column 2j in the low nibble of byte j), scales
+    fp16 [rows, ceil(cols / group)], zeros uint8 of the scales' shape or None
+    (zero point 8); weight = (code - zero) * scale.  group is 32, 64 or 128 and
+    cols a multiple of 32.  The packed copy is made once, on the current stream;
+    the inputs are not kept."""
+
+    def __init__(self, codes, scales, zeros=None, group=32):
+        if codes.dim() != 2 or scales.dim() != 2:
+            raise ValueError("codes and scales must be matrices")
+        self.rows, self.cols, self.group = codes.shape[0], 2 * codes.shape[1], int(group)
+        if self.group not in (32, 64, 128):
+            raise ValueError(f"group={group}: 32, 64 or 128")
+        if self.rows < 1 or self.cols < 32 or self.cols % 32:
+            raise ValueError(f"rows={self.rows}, cols={self.cols}: need rows >= 1 and cols a "
+                             "multiple of 32")
+        shape = (self.rows, -(-self.cols // self.group))
+        for name, t in (("scales", scales), ("zeros", zeros)):
+            if t is not None and tuple(t.shape) != shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {shape}")
+        _dev(codes, torch.uint8, "codes")
+        _dev(scales, torch.float16, "scales")
+        _dev(zeros, torch.uint8, "zeros")
+        self.device = codes.device
+        _on(self.device, scales=scales, zeros=zeros)
+        nb = int(load().spffn_q4_packed_bytes(self.rows, self.cols, self.group,
+                                              int(zeros is not None)))
+        if nb == 0:
+            raise ValueError(f"rows={self.rows}, cols={self.cols} are too large")
+        self.packed = torch.empty(nb, dtype=torch.uint8, device=self.device)
+        self.desc = Q4Desc(packed=self.packed.data_ptr(), rows=self.rows, cols=self.cols,
+                           group=self.group, zeros=int(zeros is not None))
+        self._ref = C.addressof(self.desc)
+        _call(self.device, "spffn_q4_pack", codes.data_ptr(), scales.data_ptr(), _addr(zeros),
+              self.rows, self.cols, self.group, self.packed.data_ptr())
+
+
+def q4_matvec(w, x, bias=None, resid=None, rms_eps=None, y=None):
+    """y [B, rows] = r * (W x) + bias + resid of a Q4Matrix for x [B, cols] (or
+    [cols]), B <= MAX_BATCH; r is 1, or with rms_eps the gainless RMS norm's
+    1 / sqrt(mean(x^2) + rms_eps) of each token.  y may be resid (in place)."""
+    B = _tokens(x, w.cols)
+    _size(bias, w.rows, "bias")
+    _size(resid, B * w.rows, "resid")
+    _size(y, B * w.rows, "y")
+    if rms_eps is not None and not rms_eps >= 0:
+        raise ValueError(f"rms_eps={rms_eps} must be >= 0")
+    _dev(x, torch.float32, "x")
+    _dev(bias, torch.float32, "bias")
+    _dev(resid, torch.float32, "resid")
+    if y is None:
+        y = torch.empty(x.shape[:-1] + (w.rows,), dtype=torch.float32, device=x.device)
+    _dev(y, torch.float32, "y")
+    _on(w.device, x=x, bias=bias, resid=resid, y=y)
+    _call(w.device, "spffn_q4_matvec", w._ref, x.data_ptr(), B,
+          -1.0 if rms_eps is None else float(rms_eps), _addr(bias), _addr(resid), y.data_ptr())
+    return y
+
+
+def block_tables(lens, adds, table, free_list, n_free, page_size, n_tokens, starts=None,
+                 new_lens=None, slots=None, positions=None, left=None):
+    """Page tables and slot maps of a step (all int32 on the device).
+
+    lens, adds [R]: tokens in the cache and tokens to add; table [R, width] is
+    updated in place with pages taken from the end of free_list[:n_free]; n_free
+    [1].  Returns dict(starts [R + 1], new_lens [R], slots [n_tokens], positions
+    [n_tokens], left [2] = free pages left and requests not served); slots and
+    positions are -1 from starts[R] on, slots also for requests not served."""
+    R = lens.numel()
+    if table.dim() != 2 or table.shape[0] != R:
+        raise ValueError(f"table must have shape [{R}, width], got {tuple(table.shape)}")
+    n = int(n_tokens)
+    if n < 0:
+        raise ValueError(f"n_tokens={n_tokens} < 0")
+    _size(adds, R, "adds")
+    _size(n_free, 1, "n_free")
+    sizes = (R + 1, R, n, n, 2)
+    out = [starts, new_lens, slots, positions, left]
+    names = ("starts", "new_lens", "slots", "positions", "left")
+    for name, t, k in zip(names, out, sizes):
+        _size(t, k, name)
+    for name, t in (("lens", lens), ("adds", adds), ("table", table), ("free_list", free_list),
+                    ("n_free", n_free)):
+        _dev(t, torch.int32, name)
+    dev = lens.device
+    out = [torch.empty(k, dtype=torch.int32, device=dev) if t is None else
+           _dev(t, torch.int32, name) for name, t, k in zip(names, out, sizes)]
+    ret = dict(zip(names, out))
+    _on(dev, adds=adds, table=table, free_list=free_list, n_free=n_free, **ret)
+    # an empty free list still has an address (it is never read)
+    free = free_list.data_ptr() or n_free.data_ptr()
+    _call(dev, "spffn_block_tables", lens.data_ptr(), adds.data_ptr(), R, int(page_size),
+          table.data_ptr(), table.shape[1], free, free_list.numel(), n_free.data_ptr(),
+          *(t.data_ptr() for t in out[:4]), n, out[4].data_ptr())
+    return ret
+
+
+class KVCache:
+    """A paged key/value cache of one layer: k [pages, kv_heads, head_dim / E,
+    page_size, E] and v [pages, kv_heads, page_size / E, head_dim, E] with E = 8
+    (float16) or 16 (float8_e4m3fn) elements; float8 pages come with k_scale and
+    v_scale fp32 [kv_heads], an element standing for its value times the scale
+    of its head.  The tensors are the caller's and are kept alive."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dtype not in _CACHE_DTYPES:
+            raise TypeError(f"k must be float16 or float8_e4m3fn, got {k.dtype}")
+        E = 8 if k.dtype == torch.float16 else 16
+        if k.dim() != 5 or k.shape[4] != E:
+            raise ValueError(f"k must have shape [pages, kv_heads, head_dim / {E}, page_size, {E}]")
+        self.pages, self.kv_heads, packets, self.page_size, _ = k.shape
+        self.head_dim = packets * E
+        want = (self.pages, self.kv_heads, self.page_size // E, self.head_dim, E)
+        if self.page_size not in (16, 32, 64, 128, 256):
+            raise ValueError(f"page_size={self.page_size}: a power of two in [16, 256]")
+        if self.head_dim not in (64, 96, 128, 256):
+            raise ValueError(f"head_dim={self.head_dim}: 64, 96, 128 or 256")
+        if tuple(v.shape) != want:
+            raise ValueError(f"v has shape {tuple(v.shape)}, needs {want}")
+        if (k_scale is None) != (E == 8) or (v_scale is None) != (E == 8):
+            raise ValueError("k_scale and v_scale go with a float8 cache, and only with it")
+        _size(k_scale, self.kv_heads, "k_scale")
+        _size(v_scale, self.kv_heads, "v_scale")
+        _dev(k, None, "k")
+        _dev(v, k.dtype, "v")
+        _dev(k_scale, torch.float32, "k_scale")
+        _dev(v_scale, torch.float32, "v_scale")
+        self.device = k.device
+        _on(self.device, v=v, k_scale=k_scale, v_scale=v_scale)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.desc = CacheDesc(k=k.data_ptr(), v=v.data_ptr(), k_scale=_addr(k_scale),
+                              v_scale=_addr(v_scale), pages=self.pages, page_size=self.page_size,
+                              kv_heads=self.kv_heads, head_dim=self.head_dim,
+                              dtype=_CACHE_DTYPES[k.dtype])
+        self._ref = C.addressof(self.desc)
+        self._ws = {}
+
+    def workspace_bytes(self, heads, max_new, dtype=torch.float32):
+        """Bytes of workspace a tree_attention call needs (0 on bad sizes)."""
+        key = (heads, max_new, dtype)
+        if key not in self._ws:
+            self._ws[key] = int(load().spffn_tree_attention_workspace_bytes(
+                self._ref, heads, max_new, _ROW_DTYPES.get(dtype, -1)))
+        return self._ws[key]
+
+    def workspace(self, heads, max_new, dtype=None):
+        """A workspace for tree_attention of up to max_new tokens a request and
+        queries of dtype (None: either)."""
+        n = max(self.workspace_bytes(heads, max_new, t)
+                for t in ((torch.float32, torch.float16) if dtype is None else (dtype,)))
+        if n == 0:
+            raise SpffnError(-2, "workspace", f"bad heads={heads}, max_new={max_new} or dtype")
+        return torch.empty(n, dtype=torch.uint8, device=self.device)
+
+
+def _token_rows(t, name, heads, dim):
+    """Check [N, heads, dim] rows whose tokens may be strided; the stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must have shape [N, {heads}, {dim}], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype not in _ROW_DTYPES:
+        raise TypeError(f"{name} must be float32 or float16, got {t.dtype}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def kv_append(cache, k, v, slots):
+    """Writes rows k, v [N, kv_heads, head_dim] (fp32 or fp16; the tokens may be
+    strided, as parts of a fused projection are) to the cache slots int32 [N];
+    tokens of slot -1 are skipped."""
+    ld_k = _token_rows(k, "k", cache.kv_heads, cache.head_dim)
+    ld_v = _token_rows(v, "v", cache.kv_heads, cache.head_dim)
+    N = k.shape[0]
+    if v.shape[0] != N or v.dtype != k.dtype:
+        raise ValueError("k and v must hold as many tokens of one dtype")
+    _size(slots, N, "slots")
+    _dev(slots, torch.int32, "slots")
+    _on(cache.device, k=k, v=v, slots=slots)
+    if N:
+        _call(cache.device, "spffn_kv_append", cache._ref, k.data_ptr(), v.data_ptr(),
+              _ROW_DTYPES[k.dtype], ld_k, ld_v, slots.data_ptr(), N)
+
+
+def tree_attention(cache, q, starts, lens, table, mask=None, scale=None, max_new=None, out=None,
+                   ws=None):
+    """Attention of q [N, heads, head_dim] (fp32 or fp16) over the cache, which
+    already holds the step's own tokens.  Request r's tokens are q[starts[r]:
+    starts[r + 1]], lens[r] its tokens before the step, table [R, width] its
+    pages.  mask int64 [N]: bit j lets a token see its request's token j of the
+    step (None: every token sees the ones up to itself).  max_new: the longest
+    request's token count (default: N, at most MAX_NEW).  scale defaults to
+    head_dim ** -0.5.  Returns out [N, heads, head_dim]; rows no request names
+    are left as they were."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must have shape [N, heads, head_dim]")
+    N, heads = q.shape[0], q.shape[1]
+    if heads < 1 or heads % cache.kv_heads:
+        raise ValueError(f"heads={heads} is no multiple of kv_heads={cache.kv_heads}")
+    R = lens.numel()
+    _size(starts, R + 1, "starts")
+    _size(mask, N, "mask")
+    if table.dim() != 2 or table.shape[0] != R:
+        raise ValueError(f"table must have shape [{R}, width], got {tuple(table.shape)}")
+    max_new = min(max(N, 1), MAX_NEW) if max_new is None else int(max_new)
+    ld_q = _token_rows(q, "q", heads, cache.head_dim)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    ld_out = _token_rows(out, "out", heads, cache.head_dim)
+    if out.shape[0] != N or out.dtype != q.dtype:
+        raise ValueError("out must hold as many tokens as q, of its dtype")
+    _dev(starts, torch.int32, "starts")
+    _dev(lens, torch.int32, "lens")
+    _dev(table, torch.int32, "table")
+    _dev(mask, torch.int64, "mask")
+    dev = cache.device
+    _on(dev, q=q, out=out, starts=starts, lens=lens, table=table, mask=mask)
+    if ws is None:
+        ws = cache.workspace(heads, max_new, q.dtype)
+    nb = _ws_bytes(ws, cache.workspace_bytes(heads, max_new, q.dtype))
+    _on(dev, ws=ws)
+    if N:
+        _call(dev, "spffn_tree_attention", cache._ref, q.data_ptr(), _ROW_DTYPES[q.dtype], ld_q, N,
+              heads, starts.data_ptr(), lens.data_ptr(), table.data_ptr(), R, table.shape[1],
+              _addr(mask), max_new, cache.head_dim ** -0.5 if scale is None else float(scale),
+              out.data_ptr(), ld_out, ws.data_ptr(), nb)
+    return out
 
 
 STREAM_SINK_WORDS = 4096

@@ -8,7 +8,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspffn.so")
 SOURCES = ["api.hip", "kernels_misc.hip", "kernels_gemv.hip", "kernels_ffn.hip", "kernels_b1.hip",
-           "kernels_mfma.hip"]
+           "kernels_mfma.hip", "kernels_q4mv.hip", "kernels_paged.hip", "kernels_attn.hip",
+           "kernels_attn_f16.hip", "kernels_attn_fp8.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = [

@@ -812,6 +812,234 @@ spffn_status spffn_permute_rows(const void *src, void *dst, const int32_t *perm,
     return SPFFN_OK;
 }
 
+// ---- the attention half of a decode step ------------------------------------
+
+namespace {
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+bool q4_sizes_ok(int32_t rows, int32_t cols, int32_t group) {
+    return rows >= 1 && rows <= (1 << 24) && cols >= 32 && cols <= (1 << 20) && cols % 32 == 0 &&
+           (group == 32 || group == 64 || group == 128);
+}
+
+int page_shift(int32_t page_size) {
+    for (int s = 4; s <= 8; ++s)
+        if (page_size == 1 << s) return s;
+    return -1;
+}
+
+spffn_status check_cache(const char *who, const spffn_kv_cache *c, KvCache &out) {
+    if (!c) return fail(SPFFN_E_ARG, "%s: NULL cache", who);
+    if (c->dtype != SPFFN_F16 && c->dtype != SPFFN_FP8_E4M3)
+        return fail(SPFFN_E_DTYPE, "%s: cache dtype %d (F16 or FP8_E4M3)", who, c->dtype);
+    out.fp8 = c->dtype == SPFFN_FP8_E4M3;
+    if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16))
+        return fail(SPFFN_E_ARG, "%s: cache k and v must be 16-byte aligned and not NULL", who);
+    if (out.fp8 != (c->k_scale != nullptr) || out.fp8 != (c->v_scale != nullptr))
+        return fail(SPFFN_E_ARG, "%s: k_scale and v_scale go with an fp8 cache, and only with it",
+                    who);
+    if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+        return fail(SPFFN_E_ARG, "%s: misaligned cache scale", who);
+    out.shift = page_shift(c->page_size);
+    if (out.shift < 0)
+        return fail(SPFFN_E_SHAPE, "%s: page_size=%d is no power of two in [16, 256]", who,
+                    c->page_size);
+    if (c->head_dim != 64 && c->head_dim != 96 && c->head_dim != 128 && c->head_dim != 256)
+        return fail(SPFFN_E_SHAPE, "%s: head_dim=%d (64, 96, 128 or 256)", who, c->head_dim);
+    if (c->kv_heads < 1 || c->kv_heads > 65535)
+        return fail(SPFFN_E_SHAPE, "%s: kv_heads=%d outside [1, 65535]", who, c->kv_heads);
+    if (c->pages < 1 || ((int64_t)c->pages << out.shift) >= (int64_t)1 << 31)
+        return fail(SPFFN_E_SHAPE, "%s: pages=%d of %d tokens (at least one, under 2^31 tokens)",
+                    who, c->pages, c->page_size);
+    out.k = static_cast<uint8_t *>(c->k);
+    out.v = static_cast<uint8_t *>(c->v);
+    out.ks = c->k_scale;
+    out.vs = c->v_scale;
+    out.pages = c->pages;
+    out.H = c->kv_heads;
+    out.D = c->head_dim;
+    return SPFFN_OK;
+}
+
+// A strided activation [N, row] of fp32 or fp16 elements.
+spffn_status check_rows(const char *who, const char *name, const void *p, int32_t dtype, int64_t ld,
+                        int64_t row) {
+    if (!p) return fail(SPFFN_E_ARG, "%s: %s is NULL", who, name);
+    const int es = dtype == SPFFN_F16 ? 2 : 4;
+    if (!aligned(p, 16) || ld * es % 16)
+        return fail(SPFFN_E_ARG, "%s: rows of %s must be 16-byte aligned", who, name);
+    if (ld < row || ld > (int64_t)1 << 40)
+        return fail(SPFFN_E_SHAPE, "%s: %s rows are %lld elements apart, hold %lld", who, name,
+                    (long long)ld, (long long)row);
+    return SPFFN_OK;
+}
+
+}  // namespace
+
+size_t spffn_q4_packed_bytes(int32_t rows, int32_t cols, int32_t group, int32_t zeros) {
+    return q4_sizes_ok(rows, cols, group) ? q4_packed_bytes(rows, cols, group, zeros != 0) : 0;
+}
+
+spffn_status spffn_q4_pack(const uint8_t *codes, const void *scales, const uint8_t *zeros,
+                           int32_t rows, int32_t cols, int32_t group, void *packed, void *stream) {
+    if (!codes || !scales || !packed) return fail(SPFFN_E_ARG, "q4_pack: NULL pointer");
+    if (!q4_sizes_ok(rows, cols, group))
+        return fail(SPFFN_E_SHAPE,
+                    "q4_pack: rows=%d cols=%d group=%d (cols %% 32 == 0, group 32, 64 or 128)",
+                    rows, cols, group);
+    if (!aligned(packed, 16) || !aligned(scales, 2))
+        return fail(SPFFN_E_ARG, "q4_pack: packed must be 16-byte aligned, scales 2-byte");
+    const size_t nb = q4_packed_bytes(rows, cols, group, zeros != nullptr);
+    const size_t ng = (size_t)rows * ((cols + group - 1) / group);
+    if (overlap(packed, nb, codes, (size_t)rows * (cols / 2)) || overlap(packed, nb, scales, ng * 2) ||
+        (zeros && overlap(packed, nb, zeros, ng)))
+        return fail(SPFFN_E_ARG, "q4_pack: packed overlaps an input");
+    SPFFN_HIP(launch_q4_pack(codes, static_cast<const uint16_t *>(scales), zeros, rows, cols, group,
+                             static_cast<uint8_t *>(packed), (hipStream_t)stream),
+              "4-bit pack launch");
+    return SPFFN_OK;
+}
+
+spffn_status spffn_q4_matvec(const spffn_q4_matrix *w, const float *x, int32_t B, float rms_eps,
+                             const float *bias, const float *resid, float *y, void *stream) {
+    if (!w || !w->packed || !x || !y) return fail(SPFFN_E_ARG, "q4_matvec: NULL pointer");
+    if (!q4_sizes_ok(w->rows, w->cols, w->group))
+        return fail(SPFFN_E_SHAPE,
+                    "q4_matvec: rows=%d cols=%d group=%d (cols %% 32 == 0, group 32, 64 or 128)",
+                    w->rows, w->cols, w->group);
+    if (spffn_status st = check_batch(B)) return st;
+    if (!aligned(w->packed, 16) || !aligned(x, 16) || !aligned(y, 4) || !aligned(bias, 4) ||
+        !aligned(resid, 4))
+        return fail(SPFFN_E_ARG, "q4_matvec: packed and x must be 16-byte aligned, the rest 4-byte");
+    if (rms_eps != rms_eps || std::isinf(rms_eps))
+        return fail(SPFFN_E_ARG, "q4_matvec: rms_eps must be finite");
+    const size_t ny = (size_t)B * w->rows * 4;
+    if (overlap(y, ny, x, (size_t)B * w->cols * 4))
+        return fail(SPFFN_E_ARG, "q4_matvec: y overlaps x");
+    if ((resid && resid != y && overlap(y, ny, resid, ny)) ||
+        (bias && overlap(y, ny, bias, (size_t)w->rows * 4)))
+        return fail(SPFFN_E_ARG, "q4_matvec: y overlaps bias or part of resid");
+    SPFFN_HIP(launch_q4_matvec(static_cast<const uint8_t *>(w->packed), w->rows, w->cols, w->group,
+                               w->zeros != 0, x, B, rms_eps, bias, resid, y, (hipStream_t)stream),
+              "4-bit matvec launch");
+    return SPFFN_OK;
+}
+
+spffn_status spffn_block_tables(const int32_t *lens, const int32_t *adds, int32_t R,
+                                int32_t page_size, int32_t *table, int32_t width,
+                                const int32_t *free_list, int32_t free_cap, const int32_t *n_free,
+                                int32_t *starts, int32_t *new_lens, int32_t *slots,
+                                int32_t *positions, int32_t N, int32_t *left, void *stream) {
+    const void *in[] = {lens, adds, free_list, n_free};
+    const void *out[] = {table, starts, new_lens, slots, positions, left};
+    for (const void *p : in)
+        if (!p || !aligned(p, 4)) return fail(SPFFN_E_ARG, "block_tables: NULL or misaligned input");
+    if (R < 1 || R > SPFFN_MAX_REQUESTS)
+        return fail(SPFFN_E_SHAPE, "block_tables: R=%d outside [1, %d]", R, SPFFN_MAX_REQUESTS);
+    const int shift = page_shift(page_size);
+    if (shift < 0)
+        return fail(SPFFN_E_SHAPE, "block_tables: page_size=%d is no power of two in [16, 256]",
+                    page_size);
+    if (width < 1 || free_cap < 0 || N < 0)
+        return fail(SPFFN_E_SHAPE, "block_tables: width=%d, free_cap=%d, N=%d", width, free_cap, N);
+    for (int i = 0; i < 6; ++i) {
+        const bool needed = N > 0 || (i != 3 && i != 4);  // no slots or positions without tokens
+        if ((needed && !out[i]) || !aligned(out[i], 4))
+            return fail(SPFFN_E_ARG, "block_tables: NULL or misaligned output");
+    }
+    const size_t n_in[] = {(size_t)R, (size_t)R, (size_t)free_cap, 1};
+    const size_t n_out[] = {(size_t)R * width, (size_t)R + 1, (size_t)R, (size_t)N, (size_t)N, 2};
+    for (int i = 0; i < 6; ++i) {
+        for (int j = 0; j < 4; ++j)
+            if (n_out[i] && n_in[j] && overlap(out[i], n_out[i] * 4, in[j], n_in[j] * 4))
+                return fail(SPFFN_E_ARG, "block_tables: an output overlaps an input");
+        for (int j = 0; j < i; ++j)
+            if (n_out[i] && n_out[j] && overlap(out[i], n_out[i] * 4, out[j], n_out[j] * 4))
+                return fail(SPFFN_E_ARG, "block_tables: two outputs overlap");
+    }
+    SPFFN_HIP(launch_block_tables(lens, adds, R, shift, table, width, free_list, free_cap, n_free,
+                                  starts, new_lens, slots, positions, N, left, (hipStream_t)stream),
+              "block table launch");
+    return SPFFN_OK;
+}
+
+spffn_status spffn_kv_append(const spffn_kv_cache *cache, const void *k, const void *v,
+                             int32_t dtype, int64_t ld_k, int64_t ld_v, const int32_t *slots,
+                             int32_t N, void *stream) {
+    KvCache c;
+    if (spffn_status st = check_cache("kv_append", cache, c)) return st;
+    if (dtype != SPFFN_F32 && dtype != SPFFN_F16)
+        return fail(SPFFN_E_DTYPE, "kv_append: rows of dtype %d (F32 or F16)", dtype);
+    if (N < 0) return fail(SPFFN_E_SHAPE, "kv_append: N=%d < 0", N);
+    if (N == 0) return SPFFN_OK;
+    const int64_t row = (int64_t)c.H * c.D;
+    if (spffn_status st = check_rows("kv_append", "k", k, dtype, ld_k, row)) return st;
+    if (spffn_status st = check_rows("kv_append", "v", v, dtype, ld_v, row)) return st;
+    if (!slots || !aligned(slots, 4))
+        return fail(SPFFN_E_ARG, "kv_append: NULL or misaligned slots");
+    SPFFN_HIP(launch_kv_append(c, k, v, dtype == SPFFN_F16, ld_k, ld_v, slots, N,
+                               (hipStream_t)stream),
+              "cache append launch");
+    return SPFFN_OK;
+}
+
+size_t spffn_tree_attention_workspace_bytes(const spffn_kv_cache *cache, int32_t heads,
+                                            int32_t max_new, int32_t dtype) {
+    KvCache c;
+    if (check_cache("tree_attention", cache, c) != SPFFN_OK || heads < 1 || heads % c.H ||
+        heads > 65535 || max_new < 1 || max_new > 64 || (dtype != SPFFN_F32 && dtype != SPFFN_F16))
+        return 0;
+    return attn_ws_bytes(heads, c.H, c.D, max_new, dtype == SPFFN_F16);
+}
+
+spffn_status spffn_tree_attention(const spffn_kv_cache *cache, const void *q, int32_t dtype,
+                                  int64_t ld_q, int32_t N, int32_t heads, const int32_t *starts,
+                                  const int32_t *lens, const int32_t *table, int32_t R,
+                                  int32_t width, const int64_t *mask, int32_t max_new, float scale,
+                                  void *out, int64_t ld_out, void *ws, size_t ws_bytes,
+                                  void *stream) {
+    const char *who = "tree_attention";
+    KvCache c;
+    if (spffn_status st = check_cache(who, cache, c)) return st;
+    if (dtype != SPFFN_F32 && dtype != SPFFN_F16)
+        return fail(SPFFN_E_DTYPE, "tree_attention: queries of dtype %d (F32 or F16)", dtype);
+    if (heads < 1 || heads > 65535 || heads % c.H)
+        return fail(SPFFN_E_SHAPE, "tree_attention: heads=%d is no multiple of kv_heads=%d", heads,
+                    c.H);
+    if (max_new < 1 || max_new > 64)
+        return fail(SPFFN_E_SHAPE, "tree_attention: max_new=%d outside [1, 64]", max_new);
+    if (R < 1 || R > SPFFN_MAX_REQUESTS || width < 1 || N < 0)
+        return fail(SPFFN_E_SHAPE, "tree_attention: R=%d (1..%d), width=%d, N=%d", R,
+                    SPFFN_MAX_REQUESTS, width, N);
+    // a request's work is counted in 32 bits on the device
+    const int64_t steps = (((int64_t)width << c.shift) + 31) / 32 * heads * max_new;
+    if (steps >= (int64_t)1 << 31)
+        return fail(SPFFN_E_SHAPE, "tree_attention: width=%d pages of %d tokens are too many", width,
+                    cache->page_size);
+    if (!(scale == scale) || std::isinf(scale))
+        return fail(SPFFN_E_ARG, "tree_attention: scale must be finite");
+    if (N == 0) return SPFFN_OK;
+    const int64_t row = (int64_t)heads * c.D;
+    if (spffn_status st = check_rows(who, "q", q, dtype, ld_q, row)) return st;
+    if (spffn_status st = check_rows(who, "out", out, dtype, ld_out, row)) return st;
+    const int es = dtype == SPFFN_F16 ? 2 : 4;
+    if (overlap(q, ((size_t)(N - 1) * ld_q + row) * es, out, ((size_t)(N - 1) * ld_out + row) * es))
+        return fail(SPFFN_E_ARG, "tree_attention: q and out overlap");
+    if (!starts || !lens || !table || !aligned(starts, 4) || !aligned(lens, 4) ||
+        !aligned(table, 4) || !aligned(mask, 8))
+        return fail(SPFFN_E_ARG, "tree_attention: NULL or misaligned starts, lens, table or mask");
+    const size_t need = attn_ws_bytes(heads, c.H, c.D, max_new, dtype == SPFFN_F16);
+    if (spffn_status st = check_ws(need, ws, ws_bytes)) return st;
+    AttnCall a{q, out, dtype == SPFFN_F16, ld_q, ld_out, N, heads, starts, lens, table,
+               R, width, max_new, mask, scale};
+    SPFFN_HIP(launch_tree_attention(c, a, ws, (hipStream_t)stream), "attention launch");
+    return SPFFN_OK;
+}
+
 spffn_status spffn_stream_read(const void *buf, int64_t bytes, uint32_t *sink, void *stream) {
     if (!buf || !sink) return fail(SPFFN_E_ARG, "stream_read: NULL pointer");
     if (bytes < 16 || bytes % 16)

@@ -1,0 +1,710 @@
+// Attention of drafted tokens over the paged cache (gfx950, wave64).
+//
+//   score(c, j) = scale q_c . k_j,  o_c = sum_j softmax_j(score(c, .)) v_j
+//
+// A "column" c is one query head of one drafted token; the columns that share
+// a kv head (tokens x heads per kv head) are computed together, so each key and
+// value is read from HBM once per column tile group (up to 128 columns).
+//
+// Split.  The work is cut into steps of TS tokens (32 fp16, 64 fp8) of a unit
+// (request, kv head, column tile group), and the steps of all units, laid end
+// to end, are dealt to the workgroups in equal contiguous shares.  So one long
+// request fills the chip as well as many short ones, ragged batches balance by
+// themselves, and nothing has to be known on the host: each workgroup sums the
+// lengths for itself.  A workgroup that does not cover a whole unit writes its
+// running maximum, sum and unnormalised output to a slot of the workspace
+// (at most two slots per workgroup), and a second launch joins a unit's slots in
+// order; a unit inside one workgroup is stored at once.
+//
+// Matrix products, both with the columns as the B operand (16 per instruction):
+//   S^T = K Q^T   A operand: 16 tokens x 32 dimensions, a lane's 16-byte packet
+//                 is 8 (16) dimensions of one token;
+//   O^T += V^T P^T  A operand: 16 dimensions x 32 tokens, a lane's packet is 8
+//                 (16) tokens of one dimension.
+// The cache's packet layout makes both loads 256 contiguous bytes per 16 lanes,
+// straight into registers, with no transposition and no LDS.  Token rows of S^T
+// are taken in the order that leaves a lane's scores being exactly the tokens its
+// P^T operand needs (row 4g + i of tile t is token E g + 4t + i), so the softmax
+// weights go from one product to the next without leaving their lane.
+//
+// Precision.  fp32 queries are split in hi + lo halves after a power-of-two
+// scale per column, the softmax weights likewise (2^6 above the running
+// maximum's, so that lo keeps its bits): fp32 in, fp32 out, errors near fp32's.
+// With at most 8 columns hi and lo share one instruction (columns 0..7 and
+// 8..15), otherwise they take one each into the same accumulator.  fp16 queries
+// (fp16 out) are used as they are, their weights rounded once to fp16.  Scores,
+// maxima, sums and outputs stay fp32 in registers.
+//
+// The running maximum is only raised when some score of the wave passes it by
+// 2^8 (one vote), so the usual step neither exchanges lanes nor rescales.
+#pragma once
+
+#include "device.h"
+
+namespace spffn {
+namespace attn {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kNegInf = -__builtin_inff();
+constexpr int kThreads = 256;
+
+enum Mode : int { kHalf = 0, kOne = 1, kTwo = 2 };  // columns per wave: 8, 16, 32
+
+struct Args {
+    const void *q;
+    void *out;
+    const uint8_t *k, *v;
+    const float *ks, *vs;
+    const int32_t *starts, *lens, *table;
+    const int64_t *mask;
+    float *part_o, *part_ml;
+    int64_t ldq, ldo;
+    float scale;
+    int N, R, G, H, width, pages, shift, max_new;
+    int wq;  // waves along the columns (1, 2, 4); 4 / wq along the tokens
+};
+
+// What a request asks for: committed length L, tokens T, keys tot = L + T.
+struct Req {
+    int a0, L, T, tot, steps, nqt;
+};
+
+template <int TS>
+__device__ __forceinline__ Req request(const Args &a, int r, int cw) {
+    Req q;
+    int a0 = a.starts[r], a1 = a.starts[r + 1];
+    a0 = a0 < 0 ? 0 : a0;
+    a1 = a1 > a.N ? a.N : a1;
+    int T = a1 - a0;
+    T = T < 0 ? 0 : T > a.max_new ? a.max_new : T;
+    const int64_t cap64 = (int64_t)a.width << a.shift;
+    const int cap = cap64 > 0x7FFFFF00 ? 0x7FFFFF00 : (int)cap64;
+    int L = a.lens[r];
+    L = L < 0 ? 0 : L > cap ? cap : L;
+    q.a0 = a0;
+    q.L = L;
+    q.T = T;
+    q.tot = cap - L < T ? cap : L + T;
+    q.steps = (q.tot + TS - 1) / TS;
+    q.nqt = (T * a.G + cw - 1) / cw;
+    return q;
+}
+
+// Steps of request r over all its units.
+template <int TS>
+__device__ __forceinline__ int64_t req_steps(const Args &a, int r, int cw) {
+    if (r >= a.R) return 0;
+    const Req q = request<TS>(a, r, cw);
+    return (int64_t)q.steps * q.nqt * a.H;
+}
+
+__device__ __forceinline__ int64_t scan64(int64_t v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int64_t u = __shfl_up(v, o, 64);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// Every wave computes the plan for itself: the total and each workgroup's share.
+template <int TS>
+__device__ __forceinline__ int64_t plan_total(const Args &a, int cw, int lane, int64_t &incl0) {
+    int64_t total = 0;
+    for (int b = 0; b < a.R; b += 64) {
+        const int64_t incl = scan64(req_steps<TS>(a, b + lane, cw), lane);
+        if (b == 0) incl0 = incl;
+        total += __shfl(incl, 63, 64);
+    }
+    return total;
+}
+
+// The request that holds position p < total, and its first position.
+template <int TS>
+__device__ __forceinline__ int plan_find(const Args &a, int cw, int lane, int64_t incl0, int64_t p,
+                                         int64_t &base) {
+    int64_t before = 0;
+    for (int b = 0; b < a.R; b += 64) {
+        const int64_t incl =
+            before + (b == 0 ? incl0 : scan64(req_steps<TS>(a, b + lane, cw), lane));
+        const uint64_t past = __ballot(p < incl);
+        if (past) {
+            const int i = __ffsll((long long)past) - 1;
+            base = i ? __shfl(incl, i - 1, 64) : before;
+            return b + i;
+        }
+        before = __shfl(incl, 63, 64);
+    }
+    base = 0;  // not reached for p < total
+    return 0;
+}
+
+__device__ __forceinline__ int64_t share(int64_t total, int wgs, int wk) {
+    const int64_t c = (total + wgs - 1) / wgs;
+    return (c + wk - 1) / wk * wk;
+}
+
+// Eight dimensions (tokens) of a packet as halves.
+__device__ __forceinline__ half8 fp8_half(uint32_t w0, uint32_t w1) {
+    const half2v a = __builtin_bit_cast(half2v, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, false));
+    const half2v b = __builtin_bit_cast(half2v, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, true));
+    const half2v c = __builtin_bit_cast(half2v, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, false));
+    const half2v d = __builtin_bit_cast(half2v, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, true));
+    return half8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+template <bool FP8>
+__device__ __forceinline__ half8 packet_half(const uint4 &p, int hf) {
+    if constexpr (FP8) return hf ? fp8_half(p.z, p.w) : fp8_half(p.x, p.y);
+    else return __builtin_bit_cast(half8, p);
+}
+
+__device__ __forceinline__ bool finite_half(_Float16 h) {
+    return (__builtin_bit_cast(uint16_t, h) & 0x7C00u) != 0x7C00u;
+}
+
+__device__ __forceinline__ float over_groups_max(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16, 64));
+    return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+__device__ __forceinline__ float over_groups_sum(float v) {
+    v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+}
+
+// Final value of one output element: o / l, 0 for a row that saw no key, NaN
+// for one whose every key scored -inf.
+__device__ __forceinline__ float finish(float o, float m, float l, float inv) {
+    if (m == kNegInf) return l > 0.0f ? __builtin_nanf("") : l == 0.0f ? 0.0f : l;
+    return o * inv;
+}
+
+template <bool FP8, bool Q16, int D, int MODE>
+struct Cfg {
+    static constexpr int E = FP8 ? 16 : 8;
+    static constexpr int TS = 4 * E;               // tokens per step
+    static constexpr int TT = TS / 16;             // token tiles per step
+    static constexpr int HF = E / 8;               // instructions per packet
+    static constexpr int NPK = D / E;              // packets per token
+    static constexpr int KP = (NPK + 3) / 4;       // packets per lane and tile
+    static constexpr int KS = KP * HF;             // instructions per tile
+    static constexpr int DT = D / 16;              // dimension tiles
+    static constexpr int NQ = MODE == kTwo ? 2 : 1;
+    static constexpr bool HALF = MODE == kHalf;
+    static constexpr bool SPLIT = !Q16;            // hi + lo
+    static constexpr bool LO = SPLIT && !HALF;     // lo takes instructions of its own
+    static constexpr int COLS = HALF ? 8 : 16 * NQ;  // columns per wave
+    static constexpr int PITCH = D + 4;
+};
+
+template <bool FP8, bool Q16, int D, int MODE>
+__global__ __launch_bounds__(kThreads) void attend_kernel(Args a) {
+    using C = Cfg<FP8, Q16, D, MODE>;
+    constexpr int E = C::E, TS = C::TS, TT = C::TT, HF = C::HF, KP = C::KP, DT = C::DT, NQ = C::NQ;
+    constexpr uint32_t kAll = (1u << E) - 1u;
+    extern __shared__ __align__(16) float lds[];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    const int WQ = a.wq, WK = 4 / WQ;
+    const int wq = wv & (WQ - 1), wk = wv / WQ;
+    const int cw = C::COLS * WQ;
+    const int ps = 1 << a.shift;
+
+    int64_t incl0 = 0, base;
+    const int64_t total = plan_total<TS>(a, cw, lane, incl0);
+    const int64_t per = share(total, gridDim.x, WK);
+    int64_t p = (int64_t)blockIdx.x * per;
+    const int64_t end = p + per < total ? p + per : total;
+    if (p >= end) return;
+    int r = plan_find<TS>(a, cw, lane, incl0, p, base);
+    r = __builtin_amdgcn_readfirstlane(r);
+
+    Req rq = request<TS>(a, r, cw);
+    int64_t rsteps = (int64_t)rq.steps * rq.nqt * a.H;
+    while (true) {
+        // ---- the segment: steps [s0, s1) of unit (r, h, qt) ----
+        const uint32_t rel = (uint32_t)(p - base);
+        const uint32_t unit = rel / (uint32_t)rq.steps;
+        const int s0 = (int)(rel - unit * (uint32_t)rq.steps);
+        const int s1 = end - p < rq.steps - s0 ? s0 + (int)(end - p) : rq.steps;
+        const int h = (int)(unit / (uint32_t)rq.nqt), qt = (int)(unit - (uint32_t)h * rq.nqt);
+        const int n_cols = rq.T * a.G;
+        const int col0 = (qt * WQ + wq) * C::COLS;
+        const int32_t *trow = a.table + (size_t)r * a.width;
+
+        // ---- queries as B operands ----
+        half8 qh[NQ][C::KS], ql[C::LO ? NQ : 1][C::LO ? C::KS : 1];
+        float cf[NQ];
+        uint64_t bits[NQ];
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+            const int c = col0 + (C::HALF ? (n & 7) : j * 16 + n);
+            const bool real = c < n_cols;
+            const int t = real ? c / a.G : 0, gq = real ? c - t * a.G : 0;
+            const int row = rq.a0 + t;
+            bits[j] = 0;
+            if (real) {
+                bits[j] = a.mask ? (uint64_t)a.mask[row] : (~0ull >> (63 - t));
+                const int tk = rq.tot - rq.L;
+                bits[j] &= tk <= 0 ? 0ull : (~0ull >> (64 - tk));
+            }
+            const float unit_scale = a.scale * 1.44269504088896340736f * (FP8 ? a.ks[h] : 1.0f);
+            const size_t at = (size_t)row * a.ldq + (size_t)(h * a.G + gq) * D;
+            if constexpr (Q16) {
+                const _Float16 *qp = static_cast<const _Float16 *>(a.q) + at;
+#pragma unroll
+                for (int i = 0; i < C::KS; ++i) {
+                    const int d = ((i / HF) * 4 + g) * E + (i % HF) * 8;
+                    half8 x = {0, 0, 0, 0, 0, 0, 0, 0};
+                    if (real && d < D) x = *reinterpret_cast<const half8 *>(qp + d);
+                    qh[j][i] = x;
+                }
+                cf[j] = unit_scale;
+            } else {
+                const float *qp = static_cast<const float *>(a.q) + at;
+                float x[C::KS][8];
+                float m = 0.0f, odd = 0.0f;
+#pragma unroll
+                for (int i = 0; i < C::KS; ++i) {
+                    const int d = ((i / HF) * 4 + g) * E + (i % HF) * 8;
+                    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), w = u;
+                    if (real && d < D) {
+                        u = *reinterpret_cast<const float4 *>(qp + d);
+                        w = *reinterpret_cast<const float4 *>(qp + d + 4);
+                    }
+                    x[i][0] = u.x; x[i][1] = u.y; x[i][2] = u.z; x[i][3] = u.w;
+                    x[i][4] = w.x; x[i][5] = w.y; x[i][6] = w.z; x[i][7] = w.w;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        m = fmaxf(m, fabsf(x[i][e]));
+                        odd += x[i][e] * 0.0f;  // NaN as soon as one value is not finite
+                    }
+                }
+                m = over_groups_max(m);
+                odd = over_groups_sum(odd);
+                uint32_t eb = __float_as_uint(m) >> 23;
+                eb = eb < 16 ? 16 : eb > 254 ? 254 : eb;
+                const float up = __uint_as_float((267u - eb) << 23);  // largest in [2^13, 2^14)
+                // a query that is not finite makes every score NaN
+                cf[j] = unit_scale * __uint_as_float((eb - 13u) << 23) + odd;
+#pragma unroll
+                for (int i = 0; i < C::KS; ++i) {
+                    half8 hi, lo;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float v = x[i][e] * up;
+                        hi[e] = (_Float16)v;
+                        lo[e] = (_Float16)(v - (float)hi[e]);
+                    }
+                    if constexpr (C::HALF) {
+                        qh[j][i] = n < 8 ? hi : lo;
+                    } else {
+                        qh[j][i] = hi;
+                        ql[j][i] = lo;
+                    }
+                }
+            }
+        }
+
+        f32x4 o[NQ][DT];
+        float ref[NQ], l[NQ];
+        bool seen[NQ];
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+            ref[j] = kNegInf;
+            l[j] = 0.0f;
+            seen[j] = false;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[j][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+
+        for (int st = s0 + wk; st < s1; st += WK) {
+            const int t0 = st * TS;
+            // a lane's key packets belong to token group n / 4, its value packets to group g
+            const int tk = t0 + (n >> 2) * E, tv = t0 + g * E;
+            int pk = tk < rq.tot ? trow[tk >> a.shift] : -1;
+            int pv = tv < rq.tot ? trow[tv >> a.shift] : -1;
+            const bool bad = pk < 0 || pk >= a.pages || pv < 0 || pv >= a.pages;
+            const bool masked = t0 + TS > rq.L || __any(bad);
+            const bool ok_v = pv >= 0 && pv < a.pages;
+            if (pk < 0 || pk >= a.pages) pk = 0;
+            if (!ok_v) pv = 0;
+
+            uint4 kp[TT][KP], vp[DT];
+            {
+                const u32x4_t *kb = reinterpret_cast<const u32x4_t *>(a.k) +
+                                    ((size_t)pk * a.H + h) * ((size_t)C::NPK << a.shift);
+                const int o0 = (tk & (ps - 1)) + (n & 3);
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int i = 0; i < KP; ++i) {
+                        const int pkt = i * 4 + g;
+                        u32x4_t x = {0u, 0u, 0u, 0u};
+                        if (C::NPK % 4 == 0 || pkt < C::NPK)
+                            x = kb[((size_t)pkt << a.shift) + o0 + 4 * t];
+                        kp[t][i] = __builtin_bit_cast(uint4, x);
+                    }
+                const u32x4_t *vb = reinterpret_cast<const u32x4_t *>(a.v) +
+                                    (((size_t)pv * a.H + h) * (ps / E) + (tv & (ps - 1)) / E) * D + n;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) vp[d] = __builtin_bit_cast(uint4, vb[d * 16]);
+            }
+
+            // ---- scores ----
+            f32x4 s[NQ][TT];
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) s[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int i = 0; i < C::KS; ++i) {
+                    const half8 kx = packet_half<FP8>(kp[t][i / HF], i % HF);
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) {
+                        s[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kx, qh[j][i], s[j][t], 0, 0, 0);
+                        if constexpr (C::LO)
+                            s[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kx, ql[j][i], s[j][t], 0, 0, 0);
+                    }
+                }
+            if constexpr (C::HALF) {
+                // columns n and n + 8 hold the products with hi and lo: add them
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int x = __float_as_int(s[0][t][i]);
+                        s[0][t][i] += __int_as_float(
+                            __builtin_amdgcn_update_dpp(0, x, 0x128, 0xF, 0xF, false));  // row_ror:8
+                    }
+            }
+
+            // ---- masks: a lane's scores are the E consecutive tokens from tv on ----
+            uint32_t hid[NQ];  // bit e: token tv + e does not count for this column
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) hid[j] = 0;
+            if (masked) {
+                const int jt = tv - rq.L;  // tv's place among the step's own tokens
+                const uint32_t old = jt >= 0 ? 0u : jt <= -E ? kAll : (1u << -jt) - 1u;
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    const uint64_t own = jt >= 64 || jt <= -E ? 0ull
+                                         : jt >= 0 ? bits[j] >> jt : bits[j] << -jt;
+                    hid[j] = ok_v ? ~(old | (uint32_t)own) & kAll : kAll;
+                }
+            }
+
+            // ---- softmax weights ----
+            half8 ph[NQ][HF], pl[C::LO ? NQ : 1][HF];
+            float pf[NQ][TT][4];
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+                float top = kNegInf;
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = s[j][t][i] * cf[j];
+                        top = fmaxf(top, ((hid[j] >> (4 * t + i)) & 1) ? kNegInf : x);
+                    }
+                if (__any(top > ref[j] + 8.0f)) {
+                    const float up = fmaxf(ref[j], over_groups_max(top));
+                    const float alpha = up == kNegInf ? 1.0f : exp2f(ref[j] - up);
+                    l[j] *= alpha;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) o[j][d] *= alpha;
+                    ref[j] = up;
+                }
+                seen[j] = seen[j] || hid[j] != kAll;
+                const float sub = 6.0f - (ref[j] == kNegInf ? 0.0f : ref[j]);
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float w = __builtin_amdgcn_exp2f(fmaf(s[j][t][i], cf[j], sub));
+                        if ((hid[j] >> (4 * t + i)) & 1) w = 0.0f;
+                        pf[j][t][i] = w;
+                        l[j] += w;
+                    }
+#pragma unroll
+                for (int hf = 0; hf < HF; ++hf)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float w = pf[j][2 * hf + e / 4][e % 4];
+                        const _Float16 hi = (_Float16)w;
+                        if constexpr (C::HALF) {
+                            const _Float16 lo = (_Float16)(w - (float)hi);
+                            ph[j][hf][e] = n < 8 ? hi : lo;
+                        } else {
+                            ph[j][hf][e] = hi;
+                            if constexpr (C::LO) pl[j][hf][e] = (_Float16)(w - (float)hi);
+                        }
+                    }
+            }
+
+            // ---- outputs ----
+            bool odd = false;  // some value of this step is not finite
+            if (masked) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    half8 x[HF];
+#pragma unroll
+                    for (int hf = 0; hf < HF; ++hf) {
+                        x[hf] = packet_half<FP8>(vp[d], hf);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            odd = odd || (ok_v && tv + 8 * hf + e < rq.tot && !finite_half(x[hf][e]));
+                    }
+                }
+                odd = __any(odd);
+            }
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int hf = 0; hf < HF; ++hf) {
+                    half8 vx = packet_half<FP8>(vp[d], hf);
+                    if (masked) {
+                        // tokens without a key, and values that are not finite, leave the product
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (!ok_v || tv + 8 * hf + e >= rq.tot || !finite_half(vx[e]))
+                                vx[e] = (_Float16)0.0f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) {
+                        o[j][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vx, ph[j][hf], o[j][d], 0, 0, 0);
+                        if constexpr (C::LO)
+                            o[j][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vx, pl[j][hf], o[j][d], 0, 0, 0);
+                    }
+                }
+            if (odd) {
+                // Rare: add the values that are not finite one by one, to the columns that see
+                // them only (in the product a weight of 0 would still have made NaN of them).
+                for (int tok = 0; tok < TS; ++tok) {
+                    const int gs = tok / E, e = tok % E;
+                    if (t0 + tok >= rq.tot) break;
+                    const int pg = trow[(t0 + tok) >> a.shift];
+                    if (pg < 0 || pg >= a.pages) continue;
+                    const size_t row = ((size_t)pg * a.H + h) * (ps / E) + ((t0 + tok) & (ps - 1)) / E;
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) {
+                        float w = 0.0f;
+#pragma unroll
+                        for (int t = 0; t < TT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (4 * t + i == e) w = pf[j][t][i];
+                        w = __shfl(w, gs * 16 + n, 64);
+                        const bool on = !((__shfl((int)hid[j], gs * 16 + n, 64) >> e) & 1);
+#pragma unroll
+                        for (int d = 0; d < DT; ++d)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const size_t at = (row * D + d * 16 + 4 * g + i) * E + e;
+                                float v;
+                                if constexpr (FP8)
+                                    v = (a.v[at] & 0x7F) == 0x7F ? __builtin_nanf("") : 0.0f;
+                                else v = (float)reinterpret_cast<const _Float16 *>(a.v)[at];
+                                if (on && !(fabsf(v) < __builtin_inff())) o[j][d][i] += w * v;
+                            }
+                    }
+                }
+            }
+        }
+
+        // ---- the workgroup's share of the unit ----
+        const bool whole = s0 == 0 && s1 == rq.steps;
+        float vs = FP8 ? a.vs[h] : 1.0f;
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+            l[j] = over_groups_sum(l[j]);
+            const bool any = __shfl_xor(seen[j], 16, 64) || seen[j];
+            seen[j] = __shfl_xor(any, 32, 64) || any;
+            if (ref[j] == kNegInf && l[j] == 0.0f) l[j] = seen[j] ? 1.0f : 0.0f;
+            if constexpr (C::HALF) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[j][d][i] += __int_as_float(__builtin_amdgcn_update_dpp(
+                            0, __float_as_int(o[j][d][i]), 0x128, 0xF, 0xF, false));
+            }
+        }
+        // LDS: [wave][column][D + 4], then maxima and sums [wave][column][2]
+        float *lo_ = lds + (size_t)wv * C::COLS * C::PITCH;
+        float *ml = lds + (size_t)4 * C::COLS * C::PITCH;
+        if (!C::HALF || n < 8) {
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+                const int c = j * 16 + n;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    *reinterpret_cast<f32x4 *>(lo_ + c * C::PITCH + d * 16 + 4 * g) = o[j][d];
+                if (g == 0) {
+                    ml[(wv * C::COLS + c) * 2] = ref[j];
+                    ml[(wv * C::COLS + c) * 2 + 1] = l[j];
+                }
+            }
+        }
+        __syncthreads();
+        const size_t slot = 2 * (size_t)blockIdx.x + (s0 == 0 ? 1 : 0);
+        for (int x = threadIdx.x; x < cw * (D / 4); x += kThreads) {
+            const int c = x / (D / 4), d4 = x - c * (D / 4);
+            const int w0 = c / C::COLS, cc = c - w0 * C::COLS;  // wave along the columns, its column
+            const int cg = qt * cw + c;
+            if (cg >= n_cols) break;
+            float m = kNegInf;
+            for (int kx = 0; kx < WK; ++kx) m = fmaxf(m, ml[((kx * WQ + w0) * C::COLS + cc) * 2]);
+            float sum = 0.0f;
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            for (int kx = 0; kx < WK; ++kx) {
+                const int wx = kx * WQ + w0;
+                const float mx = ml[(wx * C::COLS + cc) * 2];
+                const float f = m == kNegInf ? 1.0f : mx == kNegInf ? 0.0f : exp2f(mx - m);
+                const float lx = ml[(wx * C::COLS + cc) * 2 + 1];
+                sum += f * lx;
+                acc += f * *reinterpret_cast<const f32x4 *>(
+                               lds + ((size_t)wx * C::COLS + cc) * C::PITCH + d4 * 4);
+            }
+            if (whole) {
+                const float inv = vs / sum;
+                const int t = cg / a.G, gq = cg - t * a.G;
+                const size_t at = (size_t)(rq.a0 + t) * a.ldo + (size_t)(h * a.G + gq) * D + d4 * 4;
+                if constexpr (Q16) {
+                    half4 y;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = (_Float16)finish(acc[i], m, sum, inv);
+                    *reinterpret_cast<half4 *>(static_cast<_Float16 *>(a.out) + at) = y;
+                } else {
+                    f32x4 y;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = finish(acc[i], m, sum, inv);
+                    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = y;
+                }
+            } else {
+                *reinterpret_cast<f32x4 *>(a.part_o + (slot * cw + c) * D + d4 * 4) = acc;
+                if (d4 == 0) {
+                    a.part_ml[(slot * cw + c) * 2] = m;
+                    a.part_ml[(slot * cw + c) * 2 + 1] = sum;
+                }
+            }
+        }
+
+        // ---- next segment ----
+        p += s1 - s0;
+        if (p >= end) break;
+        __syncthreads();  // the next segment reuses the LDS
+        if (p - base >= rsteps) {
+            do {
+                base += rsteps;
+                ++r;
+                rq = request<TS>(a, r, cw);
+                rsteps = (int64_t)rq.steps * rq.nqt * a.H;
+            } while (rsteps == 0);
+        }
+    }
+}
+
+// Joins the slots of the unit that workgroup blockIdx.x of the attention
+// launch began and did not finish: slot 2w + 1 holds its first part, the
+// following workgroups' slots 2w' the rest.  One thread per four outputs of a
+// column, the parts added in order.
+template <bool FP8, bool Q16, int D, int MODE>
+__global__ __launch_bounds__(kThreads) void attend_join_kernel(Args a, int wgs) {
+    using C = Cfg<FP8, Q16, D, MODE>;
+    constexpr int TS = C::TS;
+    const int lane = threadIdx.x & 63;
+    const int WK = 4 / a.wq, cw = C::COLS * a.wq;
+    int64_t incl0 = 0, base;
+    const int64_t total = plan_total<TS>(a, cw, lane, incl0);
+    const int64_t per = share(total, wgs, WK);
+    const int w = blockIdx.x;
+    const int64_t p0 = (int64_t)w * per, end = p0 + per;
+    if (end >= total) return;  // the last workgroup with work finishes its units
+    const int r = __builtin_amdgcn_readfirstlane(plan_find<TS>(a, cw, lane, incl0, end - 1, base));
+    const Req rq = request<TS>(a, r, cw);
+    const uint32_t unit = (uint32_t)(end - 1 - base) / (uint32_t)rq.steps;
+    const int64_t u0 = base + (int64_t)unit * rq.steps, u1 = u0 + rq.steps;
+    if (u0 < p0 || u1 <= end) return;  // begun earlier, or finished here
+    const int last = (int)((u1 - 1) / per);
+    const int h = (int)(unit / (uint32_t)rq.nqt), qt = (int)(unit - (uint32_t)h * rq.nqt);
+    const int x = blockIdx.y * kThreads + threadIdx.x;
+    const int c = x / (D / 4), d4 = x - c * (D / 4);
+    const int cg = qt * cw + c;
+    if (c >= cw || cg >= rq.T * a.G) return;
+    float m = kNegInf, sum = 0.0f;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int i = w; i <= last; ++i) {
+        const size_t at = (size_t)(2 * i + (i == w ? 1 : 0)) * cw + c;
+        const float mx = a.part_ml[at * 2], lx = a.part_ml[at * 2 + 1];
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(a.part_o + at * D + d4 * 4);
+        const float top = fmaxf(m, mx);
+        const float f0 = top == kNegInf ? 1.0f : m == kNegInf ? 0.0f : exp2f(m - top);
+        const float f1 = top == kNegInf ? 1.0f : mx == kNegInf ? 0.0f : exp2f(mx - top);
+        sum = f0 * sum + f1 * lx;
+        acc = acc * f0 + v * f1;
+        m = top;
+    }
+    const float inv = (FP8 ? a.vs[h] : 1.0f) / sum;
+    const int t = cg / a.G, gq = cg - t * a.G;
+    const size_t at = (size_t)(rq.a0 + t) * a.ldo + (size_t)(h * a.G + gq) * D + d4 * 4;
+    if constexpr (Q16) {
+        half4 y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = (_Float16)finish(acc[i], m, sum, inv);
+        *reinterpret_cast<half4 *>(static_cast<_Float16 *>(a.out) + at) = y;
+    } else {
+        f32x4 y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = finish(acc[i], m, sum, inv);
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = y;
+    }
+}
+
+template <bool FP8, bool Q16, int D, int MODE>
+hipError_t launch_mode(const Args &a, int wgs, hipStream_t s) {
+    using C = Cfg<FP8, Q16, D, MODE>;
+    auto fn = attend_kernel<FP8, Q16, D, MODE>;
+    const size_t lds = (size_t)4 * C::COLS * (C::PITCH + 2) * 4;
+    if (lds > 65536) {
+        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(fn),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
+    }
+    fn<<<wgs, kThreads, lds, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int threads = C::COLS * a.wq * (D / 4);
+    attend_join_kernel<FP8, Q16, D, MODE>
+        <<<dim3(wgs, (threads + kThreads - 1) / kThreads), kThreads, 0, s>>>(a, wgs);
+    return hipGetLastError();
+}
+
+template <bool FP8, bool Q16, int D>
+hipError_t launch_dim(const Args &a, int mode, int wgs, hipStream_t s) {
+    if constexpr (D <= 128)
+        if (mode == kTwo) return launch_mode<FP8, Q16, D, kTwo>(a, wgs, s);
+    if constexpr (!Q16)
+        if (mode == kHalf) return launch_mode<FP8, Q16, D, kHalf>(a, wgs, s);
+    return launch_mode<FP8, Q16, D, kOne>(a, wgs, s);
+}
+
+template <bool FP8, bool Q16>
+hipError_t launch_all(const Args &a, int dim, int mode, int wgs, hipStream_t s) {
+    switch (dim) {
+        case 64: return launch_dim<FP8, Q16, 64>(a, mode, wgs, s);
+        case 96: return launch_dim<FP8, Q16, 96>(a, mode, wgs, s);
+        case 128: return launch_dim<FP8, Q16, 128>(a, mode, wgs, s);
+        default: return launch_dim<FP8, Q16, 256>(a, mode, wgs, s);
+    }
+}
+
+}  // namespace attn
+}  // namespace spffn

@@ -171,4 +171,45 @@ hipError_t launch_layer_b1(const Layer &L, const float *hid, const float *h, con
                            bool adapt, hipStream_t s, hipEvent_t ev_start = nullptr,
                            hipEvent_t ev_stop = nullptr);
 
+// ---- the attention half of a decode step ------------------------------------
+// 4-bit matrix with group scales (kernels_q4mv.hip)
+size_t q4_packed_bytes(int rows, int cols, int group, bool zeros);
+hipError_t launch_q4_pack(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros,
+                          int rows, int cols, int group, uint8_t *packed, hipStream_t s);
+// eps < 0: no RMS normalisation; bias, resid may be nullptr
+hipError_t launch_q4_matvec(const uint8_t *packed, int rows, int cols, int group, bool zeros,
+                            const float *x, int B, float eps, const float *bias,
+                            const float *resid, float *y, hipStream_t s);
+
+// Paged key/value cache (kernels_paged.hip); page_size = 1 << shift.
+struct KvCache {
+    uint8_t *k, *v;
+    const float *ks, *vs;  // fp8 only: a scale per kv head
+    bool fp8;
+    int pages, shift, H, D;
+};
+hipError_t launch_block_tables(const int32_t *lens, const int32_t *adds, int R, int shift,
+                               int32_t *table, int width, const int32_t *free_list, int free_cap,
+                               const int32_t *n_free, int32_t *starts, int32_t *new_lens,
+                               int32_t *slots, int32_t *positions, int N, int32_t *left,
+                               hipStream_t s);
+// ldk, ldv: elements from one token's row to the next
+hipError_t launch_kv_append(const KvCache &c, const void *k, const void *v, bool src16, int64_t ldk,
+                            int64_t ldv, const int32_t *slots, int N, hipStream_t s);
+
+// Attention over the cache (attn_tile.h).
+struct AttnCall {
+    const void *q;
+    void *out;
+    bool q16;
+    int64_t ldq, ldo;
+    int N, heads;
+    const int32_t *starts, *lens, *table;
+    int R, width, max_new;
+    const int64_t *mask;
+    float scale;
+};
+size_t attn_ws_bytes(int heads, int kv_heads, int dim, int max_new, bool q16);
+hipError_t launch_tree_attention(const KvCache &c, const AttnCall &q, void *ws, hipStream_t s);
+
 }  // namespace spffn

@@ -321,6 +321,135 @@ spffn_status spffn_graph_launch(const spffn_graph *graph, void *stream);
 
 void spffn_graph_destroy(spffn_graph *graph);
 
+/* ---- the attention half of a decode step ------------------------------- */
+
+/* Between two FFN layers of a model stands its attention: projections,
+ * the cache of earlier tokens, and the attention of the step's tokens over it.
+ * The calls below follow the conventions at the top of this file; none of them
+ * needs a backward pass (the library serves), none allocates. */
+
+/* [host] A 4-bit matrix [rows, cols] with a scale (and, with zeros != 0, a
+ * zero point) per row and group of `group` columns:
+ *   W[i][c] = (q[i][c] - z[i][c / group]) * s[i][c / group],  z = 8 without zeros.
+ * group is 32, 64 or 128; cols % 32 == 0, 32 <= cols <= 2^20 (the last group
+ * may be partial); 1 <= rows <= 2^24.  `packed` is what spffn_q4_pack wrote
+ * (BORROWED, 16-byte aligned). */
+typedef struct {
+    const void *packed;
+    int32_t rows, cols, group, zeros;
+} spffn_q4_matrix;
+
+/* Bytes of the packed form (0 on bad sizes). */
+size_t spffn_q4_packed_bytes(int32_t rows, int32_t cols, int32_t group, int32_t zeros);
+
+/* Load time: lays a matrix out for spffn_q4_matvec.  codes [rows, cols / 2]:
+ * byte j of a row holds column 2j in its low nibble and column 2j + 1 in its
+ * high nibble; scales fp16 [rows, ceil(cols / group)]; zeros uint8 of the same
+ * shape (0..15, the low four bits count) or NULL.  packed: 16-byte aligned,
+ * spffn_q4_packed_bytes(rows, cols, group, zeros != NULL) bytes, not
+ * overlapping the inputs. */
+spffn_status spffn_q4_pack(const uint8_t *codes, const void *scales, const uint8_t *zeros,
+                           int32_t rows, int32_t cols, int32_t group, void *packed, void *stream);
+
+/* y[b] = r_b * (W x[b]) + bias + resid[b] for 1 <= B <= SPFFN_MAX_BATCH tokens.
+ * x [B, cols] (16-byte aligned), y [B, rows]; bias fp32 [rows] or NULL; resid
+ * fp32 [B, rows] or NULL, and may be y itself.  rms_eps >= 0: r_b = 1 /
+ * sqrt(mean(x[b]^2) + rms_eps), the gainless RMS norm that spffn_decode_step
+ * applies before a layer; rms_eps < 0: r_b = 1.  Weights are exact (the scale
+ * is applied to a group's sum), sums are fp32 in a fixed order.  y must not
+ * overlap x. */
+spffn_status spffn_q4_matvec(const spffn_q4_matrix *w, const float *x, int32_t B, float rms_eps,
+                             const float *bias, const float *resid, float *y, void *stream);
+
+/* Block tables and slot maps of a step, from the requests' lengths.
+ *   lens  int32 [R]   tokens of each request in the cache
+ *   adds  int32 [R]   tokens this step adds to it (0 allowed)
+ *   table int32 [R, width]  pages of each request, updated in place; a page
+ *                     holds page_size tokens (a power of two, 16..256)
+ *   free_list int32 [free_cap], n_free int32 [1]: the first *n_free entries are
+ *                     free pages (not changed; the step takes them from the end)
+ * Request r needs ceil((len + add) / page_size) - ceil(len / page_size) pages.
+ * Requests are served in order: r gets its pages when the needs of requests
+ * 0..r together are at most *n_free, and is served without any when it needs
+ * none.  A request with a negative length or count, or with more tokens than
+ * its table row holds, is not served and needs nothing.  Outputs:
+ *   starts int32 [R + 1]  first token of each request in the step's batch
+ *                     (the exclusive sum of adds, served or not)
+ *   new_lens int32 [R]    len + add of a served request, len of another
+ *   slots int32 [N]   page * page_size + offset of each token's cache row; -1
+ *                     for tokens of unserved requests, for tokens on a table
+ *                     entry that is negative, and from starts[R] on
+ *   positions int32 [N]   each token's position (-1 from starts[R] on)
+ *   left int32 [2]    free pages left, and the number of unserved requests
+ * N: room of slots and positions (a batch padded to N).  1 <= R <= 4096.  The
+ * lengths and counts are inputs only: no output may alias them (SPFFN_E_ARG);
+ * the free list's new count is left[0]. */
+#define SPFFN_MAX_REQUESTS 4096
+spffn_status spffn_block_tables(const int32_t *lens, const int32_t *adds, int32_t R,
+                                int32_t page_size, int32_t *table, int32_t width,
+                                const int32_t *free_list, int32_t free_cap, const int32_t *n_free,
+                                int32_t *starts, int32_t *new_lens, int32_t *slots,
+                                int32_t *positions, int32_t N, int32_t *left, void *stream);
+
+/* [host] A paged key/value cache of one layer.  Elements are SPFFN_F16 or
+ * SPFFN_FP8_E4M3 and stored in 16-byte packets of E elements (8 or 16):
+ *   k [pages, kv_heads, head_dim / E, page_size, E]
+ *   v [pages, kv_heads, page_size / E, head_dim, E]
+ * head_dim is 64, 96, 128 or 256; page_size a power of two, 16..256;
+ * pages * page_size < 2^31.  With fp8 an element stands for its E4M3 value
+ * times k_scale[head] (v_scale[head]), fp32 [kv_heads] on the device; both are
+ * NULL for fp16.  All memory is BORROWED; k and v 16-byte aligned. */
+typedef struct {
+    void *k, *v;
+    const float *k_scale, *v_scale;
+    int32_t pages, page_size, kv_heads, head_dim;
+    int32_t dtype; /* SPFFN_F16 or SPFFN_FP8_E4M3 */
+} spffn_kv_cache;
+
+/* Writes N new rows into the cache: token n's key and value of every head to
+ * slot slots[n] (int32 [N]); a slot outside [0, pages * page_size) is skipped
+ * (a padded or unserved token).  k, v: SPFFN_F32 or SPFFN_F16 (dtype), token n
+ * at k + n * ld_k elements, its heads [kv_heads, head_dim] contiguous (parts of
+ * a wider projection are fine); rows 16-byte aligned.  Elements are rounded
+ * once: fp16 to nearest, fp8 the nearest E4M3 value of x / scale, saturating at
+ * +-448.  Rows of the cache that no slot names keep their bits.  A slot given
+ * twice ends with elements of either row. */
+spffn_status spffn_kv_append(const spffn_kv_cache *cache, const void *k, const void *v,
+                             int32_t dtype, int64_t ld_k, int64_t ld_v, const int32_t *slots,
+                             int32_t N, void *stream);
+
+/* Attention of a step's tokens (a tree of drafted tokens per request, or one
+ * token) over the cache that already holds them.
+ *   q, out [N, heads, head_dim]  SPFFN_F32 or SPFFN_F16 (dtype, both the same),
+ *              token n at q + n * ld_q elements, rows 16-byte aligned; heads a
+ *              multiple of kv_heads (query head i reads kv head i / (heads /
+ *              kv_heads)); q and out must not overlap
+ *   starts int32 [R + 1]  request r's tokens are starts[r] .. starts[r + 1]
+ *   lens int32 [R]     tokens of r in the cache before this step
+ *   table int32 [R, width]  its pages
+ *   mask int64 [N] or NULL: bit j of mask[n] lets token n see its request's
+ *              token j (itself included) of this step; NULL: tokens 0..n of
+ *              them (a chain).  Every token sees the lens[r] earlier ones.
+ *   max_new    1..64, at least the longest request's token count: tokens past
+ *              it are neither computed nor seen
+ * out = softmax(scale * q . k) v in fp32 arithmetic (fp16 queries: softmax
+ * weights rounded to fp16).  Where a token sees no key out is 0.  Tokens on
+ * pages outside [0, pages) and past the table's width are not there.  Keys and
+ * values that are not finite reach only the tokens that see them: a value makes
+ * their output in its dimension NaN or infinite, a key makes them NaN unless
+ * its score is -inf (a weight of 0).  Rows of out that no request
+ * names are left as they were.  1 <= R <= SPFFN_MAX_REQUESTS.
+ * ws: spffn_tree_attention_workspace_bytes bytes, 256-byte aligned; it holds
+ * nothing between calls, and calls that overlap need one each. */
+size_t spffn_tree_attention_workspace_bytes(const spffn_kv_cache *cache, int32_t heads,
+                                            int32_t max_new, int32_t dtype);
+spffn_status spffn_tree_attention(const spffn_kv_cache *cache, const void *q, int32_t dtype,
+                                  int64_t ld_q, int32_t N, int32_t heads, const int32_t *starts,
+                                  const int32_t *lens, const int32_t *table, int32_t R,
+                                  int32_t width, const int64_t *mask, int32_t max_new, float scale,
+                                  void *out, int64_t ld_out, void *ws, size_t ws_bytes,
+                                  void *stream);
+
 /* ---- load-time utilities ---------------------------------------------- */
 
 /* Activation profile over N tokens x [N, d] (N >= 1): counts[i] (device
