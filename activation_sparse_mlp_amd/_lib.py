@@ -87,7 +87,8 @@ SIGNATURES = {
     "spffn_q4_0_repack": (_i32, [_vp, _vp, _i32, _i32, _vp]),
     "spffn_q4_packed_bytes": (_sz, [_i32, _i32, _i32, _i32]),
     "spffn_q4_pack": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]),
-    "spffn_q4_matvec": (_i32, [_vp, _vp, _i32, _f32, _vp, _vp, _vp, _vp]),
+    "spffn_q4_matvec_workspace_bytes": (_sz, [_vp, _i32]),
+    "spffn_q4_matvec": (_i32, [_vp, _vp, _i32, _f32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "spffn_block_tables": (_i32, [_vp, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp,
                                   _vp, _i32, _vp, _vp]),
     "spffn_kv_append": (_i32, [_vp, _vp, _vp, _i32, _i64, _i64, _vp, _i32, _vp]),
@@ -667,13 +668,27 @@ class Q4Matrix:
         self._ref = C.addressof(self.desc)
         _call(self.device, "spffn_q4_pack", codes.data_ptr(), scales.data_ptr(), _addr(zeros),
               self.rows, self.cols, self.group, self.packed.data_ptr())
+        self._need = [int(load().spffn_q4_matvec_workspace_bytes(self._ref, B))
+                      for B in range(MAX_BATCH + 1)]
+
+    def workspace_bytes(self, B):
+        """Bytes of workspace q4_matvec needs for B tokens (0: none)."""
+        return self._need[B] if 0 <= B <= MAX_BATCH else 0
+
+    def workspace(self, B):
+        """A workspace for q4_matvec of up to B tokens."""
+        return torch.empty(max(256, self.workspace_bytes(B)), dtype=torch.uint8,
+                           device=self.device)
 
 
-def q4_matvec(w, x, bias=None, resid=None, rms_eps=None, y=None):
+def q4_matvec(w, x, bias=None, resid=None, rms_eps=None, y=None, ws=None):
     """y [B, rows] = r * (W x) + bias + resid of a Q4Matrix for x [B, cols] (or
     [cols]), B <= MAX_BATCH; r is 1, or with rms_eps the gainless RMS norm's
-    1 / sqrt(mean(x^2) + rms_eps) of each token.  y may be resid (in place)."""
+    1 / sqrt(mean(x^2) + rms_eps) of each token.  y may be resid (in place).
+    Three tokens and more take a workspace (w.workspace(B); made here if None)."""
     B = _tokens(x, w.cols)
+    if not 1 <= B <= MAX_BATCH:
+        raise ValueError(f"{B} tokens: 1 to {MAX_BATCH}")
     _size(bias, w.rows, "bias")
     _size(resid, B * w.rows, "resid")
     _size(y, B * w.rows, "y")
@@ -685,9 +700,14 @@ def q4_matvec(w, x, bias=None, resid=None, rms_eps=None, y=None):
     if y is None:
         y = torch.empty(x.shape[:-1] + (w.rows,), dtype=torch.float32, device=x.device)
     _dev(y, torch.float32, "y")
-    _on(w.device, x=x, bias=bias, resid=resid, y=y)
+    need = w.workspace_bytes(B)
+    if need and ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=w.device)
+    nb = _ws_bytes(ws, need) if need else 0
+    _on(w.device, x=x, bias=bias, resid=resid, y=y, ws=ws)
     _call(w.device, "spffn_q4_matvec", w._ref, x.data_ptr(), B,
-          -1.0 if rms_eps is None else float(rms_eps), _addr(bias), _addr(resid), y.data_ptr())
+          -1.0 if rms_eps is None else float(rms_eps), _addr(bias), _addr(resid), y.data_ptr(),
+          ws.data_ptr() if need else None, nb)
     return y
 
 

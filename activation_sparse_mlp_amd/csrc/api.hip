@@ -904,8 +904,14 @@ spffn_status spffn_q4_pack(const uint8_t *codes, const void *scales, const uint8
     return SPFFN_OK;
 }
 
+size_t spffn_q4_matvec_workspace_bytes(const spffn_q4_matrix *w, int32_t B) {
+    if (!w || !q4_sizes_ok(w->rows, w->cols, w->group) || B < 1 || B > SPFFN_MAX_BATCH) return 0;
+    return q4_ws_bytes(w->cols, B);
+}
+
 spffn_status spffn_q4_matvec(const spffn_q4_matrix *w, const float *x, int32_t B, float rms_eps,
-                             const float *bias, const float *resid, float *y, void *stream) {
+                             const float *bias, const float *resid, float *y, void *ws,
+                             size_t ws_bytes, void *stream) {
     if (!w || !w->packed || !x || !y) return fail(SPFFN_E_ARG, "q4_matvec: NULL pointer");
     if (!q4_sizes_ok(w->rows, w->cols, w->group))
         return fail(SPFFN_E_SHAPE,
@@ -923,8 +929,11 @@ spffn_status spffn_q4_matvec(const spffn_q4_matrix *w, const float *x, int32_t B
     if ((resid && resid != y && overlap(y, ny, resid, ny)) ||
         (bias && overlap(y, ny, bias, (size_t)w->rows * 4)))
         return fail(SPFFN_E_ARG, "q4_matvec: y overlaps bias or part of resid");
+    if (const size_t need = q4_ws_bytes(w->cols, B))
+        if (spffn_status st = check_ws(need, ws, ws_bytes)) return st;
     SPFFN_HIP(launch_q4_matvec(static_cast<const uint8_t *>(w->packed), w->rows, w->cols, w->group,
-                               w->zeros != 0, x, B, rms_eps, bias, resid, y, (hipStream_t)stream),
+                               w->zeros != 0, x, B, rms_eps, bias, resid, y, ws,
+                               (hipStream_t)stream),
               "4-bit matvec launch");
     return SPFFN_OK;
 }

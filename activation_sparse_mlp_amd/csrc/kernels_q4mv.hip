@@ -8,10 +8,14 @@
 // products run on v_mfma_f32_16x16x32_f16 for every batch, one token included:
 //
 //   * weights are the A operand.  q - z is a small integer, exact in binary16:
-//     a nibble under the exponent of 1024 reads as 1024 + q (or 1024 + 16 q),
-//     and one packed operation takes 1024 + z off (or divides by 16 and takes
-//     64 + z off), so eight codes cost nine instructions.  The scale is applied
-//     in fp32 to the product of its group, so no weight is ever rounded;
+//     a nibble under the exponent of 1024 reads as 1024 + q (or 1024 + 16 q), and
+//     one packed operation takes 1024 + z off (or divides by 16 and takes 64 + z
+//     off), so eight codes cost nine instructions.  (Leaving the constant in and
+//     taking its share of the sum off at the end would save two of them, and q as
+//     a subnormal half four; the first loses what a large activation times 16 + q
+//     rounds away where its weight is 0, the second a relative 7e-5, since the
+//     product of a subnormal drops low bits.)  The scale is applied in fp32 to a
+//     group's sum, so no weight is ever rounded;
 //   * activations are the B operand, hi + lo halves of x scaled by a power of
 //     two per token and block of 128 columns (largest magnitude in [2^14,
 //     2^15)): about 22 significant bits down to 2^-18 of the block's largest,
@@ -105,60 +109,125 @@ struct Q4Args {
     float eps;  // < 0: no normalisation
 };
 
-// Eight codes as q - z.  off = -(1024 + z), off16 = -(64 + z), both twice.
-__device__ __forceinline__ half8 widen(uint32_t w, half2v off, half2v off16) {
+// The masks of the codes' bits and the exponent of 1024, in registers whose
+// values the compiler does not see: it then makes one and-or of each use, not two
+// instructions with a literal each.
+struct CodeBits {
+    uint32_t low, high, exponent;
+    __device__ __forceinline__ CodeBits() : low(0x000F000Fu), high(0x00F000F0u), exponent(0x64006400u) {
+        asm("" : "+s"(low));
+        asm("" : "+s"(high));
+        asm("" : "+v"(exponent));
+    }
+    __device__ __forceinline__ half2v operator()(uint32_t w, uint32_t mask) const {
+        return __builtin_bit_cast(half2v, (w & mask) | exponent);
+    }
+};
+
+// What a zero point takes off 1024 + q, and off 64 + q.
+struct Offsets {
+    half2v one, sixteen;
+    template <bool ZP>
+    __device__ __forceinline__ static Offsets of(uint32_t z) {
+        const _Float16 zp = ZP ? (_Float16)(float)z : (_Float16)8.0f;
+        const _Float16 a = (_Float16)-1024.0f - zp, b = (_Float16)-64.0f - zp;
+        return Offsets{half2v{a, a}, half2v{b, b}};
+    }
+};
+
+// Eight codes as q - z.
+__device__ __forceinline__ half8 widen(uint32_t w, const CodeBits &bits, const Offsets &off) {
     const half2v sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
-    const uint32_t k1 = 0x64006400u;
     const uint32_t h = w >> 8;
-    const half2v a = __builtin_bit_cast(half2v, (w & 0x000F000Fu) | k1) + off;
-    const half2v b = __builtin_elementwise_fma(__builtin_bit_cast(half2v, (w & 0x00F000F0u) | k1),
-                                               sixteenth, off16);
-    const half2v c = __builtin_bit_cast(half2v, (h & 0x000F000Fu) | k1) + off;
-    const half2v d = __builtin_elementwise_fma(__builtin_bit_cast(half2v, (h & 0x00F000F0u) | k1),
-                                               sixteenth, off16);
-    half8 r;
-    r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1];
-    r[4] = c[0]; r[5] = c[1]; r[6] = d[0]; r[7] = d[1];
-    return r;
+    const half2v a = bits(w, bits.low) + off.one;
+    const half2v b = __builtin_elementwise_fma(bits(w, bits.high), sixteenth, off.sixteen);
+    const half2v c = bits(h, bits.low) + off.one;
+    const half2v d = __builtin_elementwise_fma(bits(h, bits.high), sixteenth, off.sixteen);
+    return half8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Magnitudes are compared as integers: one instruction each (a float maximum
+// would first quiet NaNs), and whatever is not finite sorts above the rest.
 template <int CTRL>
-__device__ __forceinline__ float dpp_max(float v) {
-    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF,
-                                                               false)));
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+    return v > o ? v : o;
 }
 
 // The largest value of each group of LPT (16, 32 or 64) lanes, in every lane of it.
 template <int LPT>
-__device__ __forceinline__ float lanes_max(float v) {
-    v = dpp_max<0xB1>(v);
-    v = dpp_max<0x4E>(v);
-    v = dpp_max<0x141>(v);
-    v = dpp_max<0x140>(v);
-    if constexpr (LPT >= 32) v = fmaxf(v, __shfl_xor(v, 16, 64));
-    if constexpr (LPT >= 64) v = fmaxf(v, __shfl_xor(v, 32, 64));
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+    v = dpp_max<0xB1>(v);   // quad_perm [1,0,3,2]
+    v = dpp_max<0x4E>(v);   // quad_perm [2,3,0,1]
+    v = dpp_max<0x141>(v);  // row_half_mirror
+    v = dpp_max<0x140>(v);  // row_mirror
+    if constexpr (LPT == 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = r[0] > r[1] ? r[0] : r[1];
+    }
+    if constexpr (LPT == 64) {
+        const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+        const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+        const uint32_t x = a > b ? a : b, y = c > d ? c : d;
+        v = x > y ? x : y;  // one value for the wave, in a scalar register
+    }
     return v;
 }
 
-// NG: groups per block (128 / group size).  WIDE: B > 8.  E: activations per
-// lane and pass (2: B = 1, 4: B = 2, 8: more), so a pass takes E / 2 tokens.
-template <int NG, bool ZP, bool WIDE, int E, int RT, int W>
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+
+constexpr uint32_t kInf = 0x7F800000u;
+
+// Scale that puts a largest magnitude m in [2^14, 2^15), and its inverse.
+__device__ __forceinline__ uint32_t scale_bits(uint32_t m) {
+    const uint32_t eb = m >> 23;
+    return eb < 16 ? 16 : eb;
+}
+__device__ __forceinline__ float scale_up(uint32_t eb) { return __uint_as_float((268u - eb) << 23); }
+__device__ __forceinline__ float scale_down(uint32_t eb) { return __uint_as_float((eb - 14u) << 23); }
+
+// hi and lo halves of v * up; an infinity or NaN has lo 0 (not inf - inf).
+__device__ __forceinline__ void split(float v, float up, bool odd, _Float16 &hi, _Float16 &lo) {
+    hi = (_Float16)(v * up);
+    lo = (_Float16)fmaf(v, up, -(float)hi);
+    if (odd && magnitude(v) >= kInf) lo = (_Float16)0.0f;
+}
+
+// Fixed-order sum over the workgroup's waves of one output: red [W][RT][16][16]
+// holds a wave's sums per column and row; TWO adds the lo halves' column b + 8.
+template <int RT, int W, bool TWO>
+__device__ __forceinline__ float sum_waves(const float *red, int b, int t, int r) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        v += red[((w * RT + t) * 16 + b) * 16 + r];
+        if (TWO) v += red[((w * RT + t) * 16 + b + 8) * 16 + r];
+    }
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// B <= 2: one launch.  A wave owns blocks wv, wv + W, ... of RT tiles, with the
+// codes of DW of them in flight, and splits those blocks' activations itself, XB
+// blocks at a time (a scale per token and block), through LDS of its own.
+// ---------------------------------------------------------------------------
+template <int NG, bool ZP, int B, int RT, int W, int DW>
 __global__ __launch_bounds__(64 * W) void q4mv_kernel(Q4Args a) {
-    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int E = 2 * B;                  // activations per lane and block
+    constexpr int XB = 4 / B;
     constexpr int LPT = kBlk / E;             // lanes per token
-    constexpr int TP = 64 / LPT;              // tokens per pass
-    constexpr int NP = WIDE ? 4 : E == 8 ? 2 : 1;
     constexpr int SPG = 4 / NG;               // instructions per group
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    constexpr int U = XB > DW ? XB : DW;
+    constexpr int AREA = 2 * B * kXPitch + 32;  // halves: hi and lo planes, factors
+    constexpr size_t STAGE = (size_t)W * XB * AREA * 2;
+    constexpr size_t RED = (size_t)W * RT * 1024 + (size_t)W * 64;
+    __shared__ __align__(16) uint8_t smem[STAGE > RED ? STAGE : RED];
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int rt0 = blockIdx.x * RT;
     const int n_rt = (a.rows + kRow - 1) / kRow;
-    const int B = a.B;
-
-    // this wave's staging area: hi and lo planes of B tokens, then 16 factors
-    _Float16 *xh = reinterpret_cast<_Float16 *>(smem) + (size_t)wv * (2 * B * kXPitch + 32);
-    _Float16 *xl = xh + B * kXPitch;
-    float *xf = reinterpret_cast<float *>(xl + B * kXPitch);
+    _Float16 *xs = reinterpret_cast<_Float16 *>(smem) + wv * XB * AREA;
 
     const uint8_t *sc_base = a.packed + (size_t)a.n_rec * 1024;
     const uint8_t *zp_base = sc_base + (size_t)a.n_rec * 32 * NG;
@@ -170,159 +239,152 @@ __global__ __launch_bounds__(64 * W) void q4mv_kernel(Q4Args a) {
         rec0[t] = (size_t)rt * a.kb_n;
     }
 
-    const int tl = lane / LPT, el = (lane % LPT) * E;  // token of a pass, first column
-    const int col_tok = WIDE ? (n < B ? n : B - 1) : ((n & 7) < B ? (n & 7) : B - 1);
-    const _Float16 *bsrc = (!WIDE && n >= 8 ? xl : xh) + col_tok * kXPitch + 8 * g;
-    const _Float16 *bsrc_lo = xl + col_tok * kXPitch + 8 * g;
+    const int tok = lane / LPT, el = (lane % LPT) * E;  // this lane's token, its first column
+    const int col_tok = (n & 7) < B ? (n & 7) : B - 1;
+    const int b_at = (n >= 8 ? B * kXPitch : 0) + col_tok * kXPitch + 8 * g;
 
+    const CodeBits bits;
     f32x4 acc[RT];
-    float ss[NP];
+    float ss = 0.0f;
 #pragma unroll
     for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int p = 0; p < NP; ++p) ss[p] = 0.0f;
 
-    uint4 cw[RT];
-    half4 cs[RT][NG];
-    uint32_t cz[RT][NG];
-    float cx[NP][E];
-    auto load = [&](int kb) {
+    uint4 cw[DW][RT];
+    half4 cs[DW][RT][NG];
+    uint32_t cz[DW][RT][NG];
+    float cx[XB][E];
+    auto load_w = [&](int st, int kb) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             const size_t rec = rec0[t] + kb;
-            cw[t] = __builtin_bit_cast(
+            cw[st][t] = __builtin_bit_cast(
                 uint4, __builtin_nontemporal_load(
                            reinterpret_cast<const u32x4_t *>(a.packed + rec * 1024) + lane));
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-                cs[t][i] = *reinterpret_cast<const half4 *>(sc_base + (rec * NG + i) * 32 + g * 8);
-                if (ZP) cz[t][i] = zp_base[(rec * NG + i) * 16 + n];
-            }
-        }
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const int tok = p * TP + tl, c = kb * kBlk + el;
-            const bool in = tok < B && c < a.cols;  // cols % 32 == 0: all E columns or none
-            const float *src = a.x + (size_t)(in ? tok : 0) * a.cols + (in ? c : 0);
-            if constexpr (E == 2) {
-                const float2 v = *reinterpret_cast<const float2 *>(src);
-                cx[p][0] = in ? v.x : 0.0f;
-                cx[p][1] = in ? v.y : 0.0f;
-            } else {
-#pragma unroll
-                for (int q = 0; q < E / 4; ++q) {
-                    const float4 v = reinterpret_cast<const float4 *>(src)[q];
-                    cx[p][4 * q + 0] = in ? v.x : 0.0f;
-                    cx[p][4 * q + 1] = in ? v.y : 0.0f;
-                    cx[p][4 * q + 2] = in ? v.z : 0.0f;
-                    cx[p][4 * q + 3] = in ? v.w : 0.0f;
-                }
+                cs[st][t][i] =
+                    *reinterpret_cast<const half4 *>(sc_base + (rec * NG + i) * 32 + g * 8);
+                if (ZP) cz[st][t][i] = zp_base[(rec * NG + i) * 16 + n];
             }
         }
     };
+    auto load_x = [&](int xb, int kb) {
+        const int c = kb * kBlk + el;
+        const bool in = c < a.cols;  // cols % 32 == 0: all E columns or none
+        const float *src = a.x + (size_t)tok * a.cols + (in ? c : 0);
+        if constexpr (E == 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(src);
+            cx[xb][0] = in ? v.x : 0.0f;
+            cx[xb][1] = in ? v.y : 0.0f;
+        } else {
+            const float4 v = *reinterpret_cast<const float4 *>(src);
+            cx[xb][0] = in ? v.x : 0.0f;
+            cx[xb][1] = in ? v.y : 0.0f;
+            cx[xb][2] = in ? v.z : 0.0f;
+            cx[xb][3] = in ? v.w : 0.0f;
+        }
+    };
 
-    if (wv < a.kb_n) load(wv);
-    for (int kb = wv; kb < a.kb_n; kb += W) {
-        uint4 w4[RT];
-        half4 s4[RT][NG];
-        uint32_t z4[RT][NG];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            w4[t] = cw[t];
+    for (int b = 0; b < XB; ++b)
+        if (wv + b * W < a.kb_n) load_x(b, wv + b * W);
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                s4[t][i] = cs[t][i];
-                if (ZP) z4[t][i] = cz[t][i];
+    for (int d = 0; d < DW; ++d)
+        if (wv + d * W < a.kb_n) load_w(d, wv + d * W);
+
+    for (int kb0 = wv; kb0 < a.kb_n; kb0 += U * W) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kb = kb0 + u * W;
+            if (kb >= a.kb_n) break;
+            if (u % XB == 0) {
+                // ---- split the next XB blocks of activations ----
+                uint32_t m[XB], top = 0;
+#pragma unroll
+                for (int b = 0; b < XB; ++b) {
+                    if (b > 0 && kb + b * W >= a.kb_n) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) cx[b][e] = 0.0f;
+                    }
+                    uint32_t v = 0;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const uint32_t q = magnitude(cx[b][e]);
+                        v = v > q ? v : q;
+                    }
+                    if (a.eps >= 0.0f) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) ss = fmaf(cx[b][e], cx[b][e], ss);
+                    }
+                    m[b] = lanes_max<LPT>(v);
+                    top = top > m[b] ? top : m[b];
+                }
+                const bool odd = __any(top >= kInf);
+                if (odd) {
+                    // an infinity or NaN: scale by the finite values
+#pragma unroll
+                    for (int b = 0; b < XB; ++b) {
+                        uint32_t v = 0;
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            const uint32_t q = magnitude(cx[b][e]);
+                            v = q < kInf && q > v ? q : v;
+                        }
+                        m[b] = lanes_max<LPT>(v);
+                    }
+                }
+                __builtin_amdgcn_wave_barrier();  // the blocks before have been read
+#pragma unroll
+                for (int b = 0; b < XB; ++b) {
+                    _Float16 *xh = xs + b * AREA, *xl = xh + B * kXPitch;
+                    const uint32_t eb = scale_bits(m[b]);
+                    const float up = scale_up(eb);
+                    _Float16 hi[E], lo[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) split(cx[b][e], up, odd, hi[e], lo[e]);
+                    if constexpr (E == 2) {
+                        *reinterpret_cast<half2v *>(xh + tok * kXPitch + el) = half2v{hi[0], hi[1]};
+                        *reinterpret_cast<half2v *>(xl + tok * kXPitch + el) = half2v{lo[0], lo[1]};
+                    } else {
+                        *reinterpret_cast<half4 *>(xh + tok * kXPitch + el) =
+                            half4{hi[0], hi[1], hi[2], hi[3]};
+                        *reinterpret_cast<half4 *>(xl + tok * kXPitch + el) =
+                            half4{lo[0], lo[1], lo[2], lo[3]};
+                    }
+                    if (el == 0) reinterpret_cast<float *>(xl + B * kXPitch)[tok] = scale_down(eb);
+                }
+#pragma unroll
+                for (int b = 0; b < XB; ++b)
+                    if (kb + (XB + b) * W < a.kb_n) load_x(b, kb + (XB + b) * W);
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
             }
+            const _Float16 *xh = xs + (u % XB) * AREA;
+            half8 bx[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                bx[w] = *reinterpret_cast<const half8 *>(xh + b_at + 32 * w);
+            const float f = reinterpret_cast<const float *>(xh + 2 * B * kXPitch)[col_tok];
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                const uint4 q = cw[u % DW][t];
+                const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    const Offsets off = Offsets::of<ZP>(cz[u % DW][t][i]);
+                    f32x4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int w = i * SPG; w < (i + 1) * SPG; ++w)
+                        z = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen(words[w], bits, off), bx[w], z,
+                                                                   0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[t][j] = fmaf(z[j], fmaf((float)cs[u % DW][t][i][j], f, 0.0f), acc[t][j]);
+                }
+            }
+            if (kb + DW * W < a.kb_n) load_w(u % DW, kb + DW * W);
         }
-        // ---- split this block's activations into the wave's LDS planes ----
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const int tok = p * TP + tl;
-            float m = 0.0f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                m = fmaxf(m, fabsf(cx[p][e]));
-                ss[p] = fmaf(cx[p][e], cx[p][e], ss[p]);
-            }
-            m = lanes_max<LPT>(m);
-            const bool inf = __float_as_uint(m) >= 0x7F800000u;
-            if (__any(inf)) {
-                // an infinity: scale by the finite values, and keep it out of lo
-                float f = 0.0f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float v = fabsf(cx[p][e]);
-                    f = fmaxf(f, v < __builtin_inff() ? v : 0.0f);
-                }
-                f = lanes_max<LPT>(f);
-                if (inf) m = f;
-            }
-            uint32_t eb = __float_as_uint(m) >> 23;
-            eb = eb < 16 ? 16 : eb;
-            const float up = __uint_as_float((268u - eb) << 23);
-            if (tok < B) {
-                _Float16 hi[E], lo[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float v = cx[p][e] * up;
-                    hi[e] = (_Float16)v;
-                    const float rest = v - (float)hi[e];
-                    lo[e] = (_Float16)(fabsf(v) < __builtin_inff() ? rest : 0.0f);
-                }
-                _Float16 *dh = xh + tok * kXPitch + el, *dl = xl + tok * kXPitch + el;
-                if constexpr (E == 2) {
-                    *reinterpret_cast<half2v *>(dh) = half2v{hi[0], hi[1]};
-                    *reinterpret_cast<half2v *>(dl) = half2v{lo[0], lo[1]};
-                } else if constexpr (E == 4) {
-                    *reinterpret_cast<half4 *>(dh) = half4{hi[0], hi[1], hi[2], hi[3]};
-                    *reinterpret_cast<half4 *>(dl) = half4{lo[0], lo[1], lo[2], lo[3]};
-                } else {
-                    *reinterpret_cast<half8 *>(dh) =
-                        half8{hi[0], hi[1], hi[2], hi[3], hi[4], hi[5], hi[6], hi[7]};
-                    *reinterpret_cast<half8 *>(dl) =
-                        half8{lo[0], lo[1], lo[2], lo[3], lo[4], lo[5], lo[6], lo[7]};
-                }
-                if (el == 0) xf[tok] = __uint_as_float((eb - 14u) << 23);
-            }
-        }
-        if (kb + W < a.kb_n) load(kb + W);
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        half8 bh[4], bl[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            bh[w] = *reinterpret_cast<const half8 *>(bsrc + 32 * w);
-            if (WIDE) bl[w] = *reinterpret_cast<const half8 *>(bsrc_lo + 32 * w);
-        }
-        const float f = xf[col_tok];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            const uint32_t words[4] = {w4[t].x, w4[t].y, w4[t].z, w4[t].w};
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                half2v off = {(_Float16)-1032.0f, (_Float16)-1032.0f};
-                half2v off16 = {(_Float16)-72.0f, (_Float16)-72.0f};
-                if (ZP) {
-                    const _Float16 zp = (_Float16)(float)z4[t][i];
-                    off = half2v{(_Float16)-1024.0f - zp, (_Float16)-1024.0f - zp};
-                    off16 = half2v{(_Float16)-64.0f - zp, (_Float16)-64.0f - zp};
-                }
-                f32x4 z = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int w = i * SPG; w < (i + 1) * SPG; ++w) {
-                    const half8 aw = widen(words[w], off, off16);
-                    z = __builtin_amdgcn_mfma_f32_16x16x32_f16(aw, bh[w], z, 0, 0, 0);
-                    if (WIDE) z = __builtin_amdgcn_mfma_f32_16x16x32_f16(aw, bl[w], z, 0, 0, 0);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    acc[t][j] = fmaf(z[j], (float)s4[t][i][j] * f, acc[t][j]);
-                }
-            }
-        }
-        __builtin_amdgcn_wave_barrier();  // the next block's split overwrites these planes
     }
 
     // ---- fixed-order sum over the workgroup's waves, scale, bias, residual ----
@@ -334,24 +396,15 @@ __global__ __launch_bounds__(64 * W) void q4mv_kernel(Q4Args a) {
         *reinterpret_cast<f32x4 *>(red + ((wv * RT + t) * 16 + n) * 16 + 4 * g) = acc[t];
     if (a.eps >= 0.0f) {
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            float v = ss[p];
-            for (int o = 1; o < LPT; o <<= 1) v += __shfl_xor(v, o, 64);
-            const int tok = p * TP + tl;
-            if (el == 0 && tok < B) sq[wv * 16 + tok] = v;
-        }
+        for (int o = 1; o < LPT; o <<= 1) ss += __shfl_xor(ss, o, 64);
+        if (el == 0) sq[wv * 16 + tok] = ss;
     }
     __syncthreads();
     for (int o = tid; o < RT * kRow * B; o += 64 * W) {
-        const int b = o / (RT * kRow), lr = o - b * (RT * kRow), t = lr >> 4, r = lr & 15;
+        const int b = o / (RT * kRow), lr = o - b * (RT * kRow);
         const int row = rt0 * kRow + lr;
         if (row >= a.rows) continue;
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            v += red[((w * RT + t) * 16 + b) * 16 + r];
-            if (!WIDE) v += red[((w * RT + t) * 16 + b + 8) * 16 + r];
-        }
+        float v = sum_waves<RT, W, true>(red, b, lr >> 4, lr & 15);
         if (a.eps >= 0.0f) {
             float q = 0.0f;
 #pragma unroll
@@ -365,37 +418,258 @@ __global__ __launch_bounds__(64 * W) void q4mv_kernel(Q4Args a) {
     }
 }
 
-template <int NG, bool ZP, bool WIDE, int E, int RT, int W>
+// ---------------------------------------------------------------------------
+// B > 2: splitting the activations costs a wave more than the codes of one tile
+// do (16 tokens: 160 instructions a block against 50), so a first launch does it
+// once, one workgroup per token: the row's largest magnitude gives the token's
+// scale, the halves go to the workspace in the order of the B operand -- block,
+// instruction, [hi, lo for B > 8], lane, 16 bytes -- and the factor that undoes
+// the scale, with the RMS norm in it, behind them.
+// ---------------------------------------------------------------------------
+constexpr int kSplitThreads = 1024;
+
+struct SplitArgs {
+    const float *x;
+    _Float16 *xp;
+    float *fac;
+    int cols, kb_n, wide;
+    float eps;
+};
+
+__global__ __launch_bounds__(kSplitThreads) void q4_split_kernel(SplitArgs a) {
+    __shared__ uint32_t mx[kSplitThreads / 64];
+    __shared__ float sq[kSplitThreads / 64];
+    const int tok = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    const float *x = a.x + (size_t)tok * a.cols;
+    constexpr int KEEP = 2;  // packets of 8 a thread keeps (16384 columns), the rest is read twice
+    float keep[KEEP][8];
+    uint32_t m = 0;
+    bool odd = false;
+    float ss = 0.0f;
+    const int n_pk = a.cols / 8;
+    int i = 0;
+    for (int p = tid; p < n_pk; p += kSplitThreads, ++i) {
+        const float4 u = reinterpret_cast<const float4 *>(x)[2 * p];
+        const float4 v = reinterpret_cast<const float4 *>(x)[2 * p + 1];
+        const float e[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t q = magnitude(e[k]);
+            odd = odd || q >= kInf;
+            m = q < kInf && q > m ? q : m;
+            ss = fmaf(e[k], e[k], ss);
+        }
+#pragma unroll
+        for (int s = 0; s < KEEP; ++s)
+            if (s == i) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) keep[s][k] = e[k];
+            }
+    }
+    m = lanes_max<64>(m);
+    ss = wave_sum(ss);
+    if (lane == 0) {
+        mx[wv] = m;
+        sq[wv] = ss;
+    }
+    __syncthreads();
+    ss = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kSplitThreads / 64; ++w) {
+        m = mx[w] > m ? mx[w] : m;
+        ss += sq[w];
+    }
+    const uint32_t eb = scale_bits(m);
+    const float up = scale_up(eb);
+    if (tid == 0) {
+        const float r = a.eps >= 0.0f ? 1.0f / sqrtf(ss / (float)a.cols + a.eps) : 1.0f;
+        a.fac[2 * tok] = scale_down(eb);
+        a.fac[2 * tok + 1] = r;
+    }
+    i = 0;
+    // columns past cols (the last block's end) are zeros
+    for (int p = tid; p < a.kb_n * (kBlk / 8); p += kSplitThreads, ++i) {
+        float e[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (i < KEEP && p < n_pk) {
+#pragma unroll
+            for (int s = 0; s < KEEP; ++s)
+                if (s == i) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) e[k] = keep[s][k];
+                }
+        } else if (p < n_pk) {
+            const float4 u = reinterpret_cast<const float4 *>(x)[2 * p];
+            const float4 v = reinterpret_cast<const float4 *>(x)[2 * p + 1];
+            e[0] = u.x; e[1] = u.y; e[2] = u.z; e[3] = u.w;
+            e[4] = v.x; e[5] = v.y; e[6] = v.z; e[7] = v.w;
+        }
+        half8 hi, lo;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            _Float16 h, l;
+            split(e[k], up, odd, h, l);
+            hi[k] = h;
+            lo[k] = l;
+        }
+        // packet p holds columns 8p ..: instruction p / 4 (of 32 columns), lane group p % 4
+        const size_t at = (size_t)(p >> 2) * (a.wide ? 128 : 64) + (p & 3) * 16 + tok;
+        reinterpret_cast<half8 *>(a.xp)[at] = hi;
+        reinterpret_cast<half8 *>(a.xp)[at + (a.wide ? 64 : 8)] = lo;
+    }
+}
+
+// The product itself: as q4mv_kernel, with the B operand loaded as it is (from
+// L2: every workgroup reads it, once per RT tiles) and one scale per token, so
+// that a group's scale is one mixed-precision multiply-add per output.
+struct MmArgs {
+    Q4Args q;
+    const _Float16 *xp;
+    const float *fac;
+};
+
+template <int NG, bool ZP, bool WIDE, int RT, int W, int DW>
+__global__ __launch_bounds__(64 * W) void q4mm_kernel(MmArgs ma) {
+    const Q4Args &a = ma.q;
+    constexpr int SPG = 4 / NG, PL = WIDE ? 2 : 1;
+    __shared__ __align__(16) float red[W * RT * 256];  // [W][RT][16 columns][16 rows]
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    const int rt0 = blockIdx.x * RT;
+    const int n_rt = (a.rows + kRow - 1) / kRow;
+    const uint8_t *sc_base = a.packed + (size_t)a.n_rec * 1024;
+    const uint8_t *zp_base = sc_base + (size_t)a.n_rec * 32 * NG;
+    size_t rec0[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int rt = rt0 + t < n_rt ? rt0 + t : n_rt - 1;  // a tile past the end is not stored
+        rec0[t] = (size_t)rt * a.kb_n;
+    }
+    const CodeBits bits;
+    f32x4 acc[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    uint4 cw[DW][RT];
+    half4 cs[DW][RT][NG];
+    uint32_t cz[DW][RT][NG];
+    half8 cx[4][PL];
+    auto load_w = [&](int st, int kb) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            const size_t rec = rec0[t] + kb;
+            cw[st][t] = __builtin_bit_cast(
+                uint4, __builtin_nontemporal_load(
+                           reinterpret_cast<const u32x4_t *>(a.packed + rec * 1024) + lane));
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                cs[st][t][i] =
+                    *reinterpret_cast<const half4 *>(sc_base + (rec * NG + i) * 32 + g * 8);
+                if (ZP) cz[st][t][i] = zp_base[(rec * NG + i) * 16 + n];
+            }
+        }
+    };
+    auto load_x = [&](int w, int kb) {
+        const half8 *xp = reinterpret_cast<const half8 *>(ma.xp) + ((size_t)kb * 4 + w) * PL * 64 + lane;
+#pragma unroll
+        for (int p = 0; p < PL; ++p) cx[w][p] = xp[p * 64];
+    };
+    if (wv < a.kb_n) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) load_x(w, wv);
+    }
+#pragma unroll
+    for (int d = 0; d < DW; ++d)
+        if (wv + d * W < a.kb_n) load_w(d, wv + d * W);
+    for (int kb0 = wv; kb0 < a.kb_n; kb0 += DW * W) {
+#pragma unroll
+        for (int u = 0; u < DW; ++u) {
+            const int kb = kb0 + u * W;
+            if (kb >= a.kb_n) break;
+            const int kx = kb + W < a.kb_n ? kb + W : kb;  // the last block's are loaded again
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                f32x4 z[RT];
+#pragma unroll
+                for (int t = 0; t < RT; ++t) z[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int w = i * SPG; w < (i + 1) * SPG; ++w) {
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        const uint4 q = cw[u][t];
+                        const uint32_t word = w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w;
+                        const half8 aw = widen(word, bits, Offsets::of<ZP>(cz[u][t][i]));
+#pragma unroll
+                        for (int p = 0; p < PL; ++p)
+                            z[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(aw, cx[w][p], z[t], 0, 0, 0);
+                    }
+                    load_x(w, kx);  // for the next block, in place
+                }
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[t][j] = fmaf(z[t][j], (float)cs[u][t][i][j], acc[t][j]);
+            }
+            if (kb + DW * W < a.kb_n) load_w(u, kb + DW * W);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+        *reinterpret_cast<f32x4 *>(red + ((wv * RT + t) * 16 + n) * 16 + 4 * g) = acc[t];
+    __syncthreads();
+    for (int o = tid; o < RT * kRow * a.B; o += 64 * W) {
+        const int b = o / (RT * kRow), lr = o - b * (RT * kRow);
+        const int row = rt0 * kRow + lr;
+        if (row >= a.rows) continue;
+        float v = sum_waves<RT, W, !WIDE>(red, b, lr >> 4, lr & 15) * ma.fac[2 * b] * ma.fac[2 * b + 1];
+        if (a.bias) v += a.bias[row];
+        const size_t at = (size_t)b * a.rows + row;
+        if (a.resid) v += a.resid[at];
+        a.y[at] = v;
+    }
+}
+
+template <int NG, bool ZP, int B, int RT, int W, int DW>
 hipError_t launch_q4mv_one(const Q4Args &a, hipStream_t s) {
     const int n_rt = (a.rows + kRow - 1) / kRow;
-    const size_t stage = (size_t)W * (2 * a.B * kXPitch + 32) * 2;
-    const size_t red = (size_t)W * RT * 1024 + (size_t)W * 64;
-    const size_t lds = stage > red ? stage : red;
-    auto fn = q4mv_kernel<NG, ZP, WIDE, E, RT, W>;
-    if (lds > 65536) {
-        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(fn),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-        if (e != hipSuccess) return e;
-    }
-    fn<<<(n_rt + RT - 1) / RT, 64 * W, lds, s>>>(a);
+    q4mv_kernel<NG, ZP, B, RT, W, DW><<<(n_rt + RT - 1) / RT, 64 * W, 0, s>>>(a);
     return hipGetLastError();
 }
 
-template <int NG, bool ZP, int RT, int W>
-hipError_t launch_q4mv_b(const Q4Args &a, hipStream_t s) {
-    if (a.B > 8) return launch_q4mv_one<NG, ZP, true, 8, RT, W>(a, s);
-    if (a.B > 2) return launch_q4mv_one<NG, ZP, false, 8, RT, W>(a, s);
-    if (a.B == 2) return launch_q4mv_one<NG, ZP, false, 4, RT, W>(a, s);
-    return launch_q4mv_one<NG, ZP, false, 2, RT, W>(a, s);
+template <int NG, bool ZP, bool WIDE, int RT, int W, int DW>
+hipError_t launch_q4mm_one(const MmArgs &a, hipStream_t s) {
+    const int n_rt = (a.q.rows + kRow - 1) / kRow;
+    q4mm_kernel<NG, ZP, WIDE, RT, W, DW><<<(n_rt + RT - 1) / RT, 64 * W, 0, s>>>(a);
+    return hipGetLastError();
 }
 
-template <int RT, int W>
-hipError_t launch_q4mv_g(const Q4Args &a, int group, bool zp, hipStream_t s) {
-    switch (group) {
-        case 32: return zp ? launch_q4mv_b<4, true, RT, W>(a, s) : launch_q4mv_b<4, false, RT, W>(a, s);
-        case 64: return zp ? launch_q4mv_b<2, true, RT, W>(a, s) : launch_q4mv_b<2, false, RT, W>(a, s);
-        default: return zp ? launch_q4mv_b<1, true, RT, W>(a, s) : launch_q4mv_b<1, false, RT, W>(a, s);
-    }
+size_t split_bytes(int cols, int B) {
+    return (size_t)((cols + kBlk - 1) / kBlk) * (B > 8 ? 8192 : 4096);
+}
+
+MmArgs split_args(const Q4Args &a, void *ws) {
+    return MmArgs{a, static_cast<const _Float16 *>(ws),
+                  reinterpret_cast<const float *>(static_cast<const uint8_t *>(ws) +
+                                                  split_bytes(a.cols, a.B))};
+}
+
+hipError_t launch_q4_split(const Q4Args &a, void *ws, hipStream_t s) {
+    SplitArgs sa{a.x, static_cast<_Float16 *>(ws),
+                 reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + split_bytes(a.cols, a.B)),
+                 a.cols, a.kb_n, a.B > 8, a.eps};
+    q4_split_kernel<<<a.B, kSplitThreads, 0, s>>>(sa);
+    return hipGetLastError();
+}
+
+template <int NG, bool ZP>
+hipError_t launch_q4_shape(const Q4Args &a, void *ws, hipStream_t s) {
+    if (a.B == 1) return launch_q4mv_one<NG, ZP, 1, 1, 8, 2>(a, s);
+    if (a.B == 2) return launch_q4mv_one<NG, ZP, 2, 1, 8, 2>(a, s);
+    hipError_t e = launch_q4_split(a, ws, s);
+    if (e != hipSuccess) return e;
+    const MmArgs m = split_args(a, ws);
+    if (a.B <= 8) return launch_q4mm_one<NG, ZP, false, 2, 4, 2>(m, s);
+    return launch_q4mm_one<NG, ZP, true, 4, 4, 2>(m, s);
 }
 
 int64_t q4_records(int rows, int cols) {
@@ -416,16 +690,18 @@ hipError_t launch_q4_pack(const uint8_t *codes, const uint16_t *scales, const ui
     return hipGetLastError();
 }
 
+size_t q4_ws_bytes(int cols, int B) { return B <= 2 ? 0 : split_bytes(cols, B) + 256; }
+
 hipError_t launch_q4_matvec(const uint8_t *packed, int rows, int cols, int group, bool zeros,
                             const float *x, int B, float eps, const float *bias,
-                            const float *resid, float *y, hipStream_t s) {
-    const int n_rt = (rows + kRow - 1) / kRow;
-    Q4Args a{packed, x, bias, resid, y, rows, cols, (cols + kBlk - 1) / kBlk, B,
-             q4_records(rows, cols), eps};
-    // two tiles per wave halve the work of splitting the activations; one tile
-    // per wave where two would leave compute units without a workgroup
-    if (n_rt >= 512) return launch_q4mv_g<2, 8>(a, group, zeros, s);
-    return launch_q4mv_g<1, 8>(a, group, zeros, s);
+                            const float *resid, float *y, void *ws, hipStream_t s) {
+    const Q4Args a{packed, x, bias, resid, y, rows, cols, (cols + kBlk - 1) / kBlk, B,
+                   q4_records(rows, cols), eps};
+    switch (group) {
+        case 32: return zeros ? launch_q4_shape<4, true>(a, ws, s) : launch_q4_shape<4, false>(a, ws, s);
+        case 64: return zeros ? launch_q4_shape<2, true>(a, ws, s) : launch_q4_shape<2, false>(a, ws, s);
+        default: return zeros ? launch_q4_shape<1, true>(a, ws, s) : launch_q4_shape<1, false>(a, ws, s);
+    }
 }
 
 }  // namespace spffn

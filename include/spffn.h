@@ -356,10 +356,15 @@ spffn_status spffn_q4_pack(const uint8_t *codes, const void *scales, const uint8
  * fp32 [B, rows] or NULL, and may be y itself.  rms_eps >= 0: r_b = 1 /
  * sqrt(mean(x[b]^2) + rms_eps), the gainless RMS norm that spffn_decode_step
  * applies before a layer; rms_eps < 0: r_b = 1.  Weights are exact (the scale
- * is applied to a group's sum), sums are fp32 in a fixed order.  y must not
- * overlap x. */
+ * is applied to a group's sum), sums are fp32 in a fixed order.  A token whose
+ * activations are not all finite gets NaN or infinities, the others are as
+ * without it.  y must not overlap x.  ws: spffn_q4_matvec_workspace_bytes bytes, 256-byte aligned (none,
+ * and ws ignored, for B <= 2; 0 on bad input too); it holds nothing between
+ * calls, and calls that overlap need one each. */
+size_t spffn_q4_matvec_workspace_bytes(const spffn_q4_matrix *w, int32_t B);
 spffn_status spffn_q4_matvec(const spffn_q4_matrix *w, const float *x, int32_t B, float rms_eps,
-                             const float *bias, const float *resid, float *y, void *stream);
+                             const float *bias, const float *resid, float *y, void *ws,
+                             size_t ws_bytes, void *stream);
 
 /* Block tables and slot maps of a step, from the requests' lengths.
  *   lens  int32 [R]   tokens of each request in the cache

@@ -24,11 +24,11 @@ def q4(**kw):
 
 
 def matvec(w=None, **kw):
-    a = dict(x=at(1), B=2, eps=-1.0, bias=None, resid=None, y=at(2))
+    a = dict(x=at(1), B=2, eps=-1.0, bias=None, resid=None, y=at(2), ws=at(4), nb=1 << 20)
     a.update(kw)
     w = q4() if w is None else w
     return spffn.load().spffn_q4_matvec(C.byref(w), a["x"], a["B"], a["eps"], a["bias"],
-                                        a["resid"], a["y"], None)
+                                        a["resid"], a["y"], a["ws"], a["nb"], None)
 
 
 @pytest.mark.parametrize("status,call", [
@@ -51,6 +51,9 @@ def matvec(w=None, **kw):
     (E_ARG, lambda: matvec(bias=at(3) + 2)),
     (E_ARG, lambda: matvec(eps=float("nan"))),
     (E_ARG, lambda: matvec(eps=float("inf"))),
+    (E_WORKSPACE, lambda: matvec(B=3, ws=None)),
+    (E_WORKSPACE, lambda: matvec(B=3, nb=4096)),
+    (E_ARG, lambda: matvec(B=9, ws=at(4) + 64)),
 ])
 def test_matvec(status, call):
     assert call() == status
@@ -73,6 +76,14 @@ def test_pack():
     nb = lib.spffn_q4_packed_bytes
     assert nb(1, 32, 128, 0) == 1024 + 32 and nb(17, 160, 32, 1) == 4 * (1024 + 4 * 48)
     assert nb(0, 32, 32, 0) == nb(1, 40, 32, 0) == nb(1, 32, 8, 0) == 0
+
+
+def test_matvec_workspace_bytes():
+    nb = spffn.load().spffn_q4_matvec_workspace_bytes
+    w = C.byref(q4())
+    assert nb(w, 1) == nb(w, 2) == nb(w, 0) == nb(w, 17) == nb(None, 3) == 0
+    assert 0 < nb(w, 3) == nb(w, 8) < nb(w, 9) == nb(w, 16)
+    assert nb(C.byref(q4(cols=40)), 4) == 0
 
 
 def tables(**kw):
@@ -209,10 +220,12 @@ def test_q4_matrix_needs_a_device():
 
 class FakeMatrix:
     rows, cols, device = 8, 64, torch.device("cuda:0")
+    workspace_bytes = staticmethod(lambda B: 0)
 
 
 @pytest.mark.parametrize("x,kw", [
-    (torch.zeros(2, 65), {}), (torch.zeros(2, 2, 64), {}),
+    (torch.zeros(2, 65), {}), (torch.zeros(2, 2, 64), {}), (torch.zeros(17, 64), {}),
+    (torch.zeros(0, 64), {}),
     (torch.zeros(2, 64), dict(bias=torch.zeros(9))),
     (torch.zeros(2, 64), dict(resid=torch.zeros(8))),
     (torch.zeros(2, 64), dict(y=torch.zeros(2, 9))),

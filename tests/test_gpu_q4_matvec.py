@@ -78,14 +78,18 @@ def test_tokens_do_not_depend_on_each_other():
     x[8, 40:80] = float("-inf")
     x[9] *= 1e-44  # subnormal
     y, bound = ref.q4_matvec(wd, x)
-    # subnormal products are within a few of the smallest steps besides
+    # any_odd: an infinity times the code and times the zero point are separate sums, and
+    # inf - inf is NaN: which of the two comes out is not fixed, that it is not finite is.
+    # Subnormal products are within a few of the smallest steps besides.
     bound = bound + cols * 2.0 ** -149 * 16
     for B in (16, 8):
         xs = x[:B] if B == 16 else x[2:10]
         ys, bs = (y[:B], bound[:B]) if B == 16 else (y[2:10], bound[2:10])
-        ref.close(spffn.q4_matvec(w, xs.contiguous().to(DEV)).cpu(), ys, bs)
+        ref.close(spffn.q4_matvec(w, xs.contiguous().to(DEV)).cpu(), ys, bs,
+                  any_odd=True)
     for b in range(16):  # one token alone
-        ref.close(spffn.q4_matvec(w, x[b].to(DEV)).cpu()[None], y[b:b + 1], bound[b:b + 1])
+        ref.close(spffn.q4_matvec(w, x[b].to(DEV)).cpu()[None], y[b:b + 1], bound[b:b + 1],
+                  any_odd=True)
 
 
 def test_small_values_next_to_an_outlier():
