@@ -144,9 +144,13 @@ __device__ __forceinline__ int plan_find(const Args &a, int cw, int lane, int64_
     return 0;
 }
 
-__device__ __forceinline__ int64_t share(int64_t total, int wgs, int wk) {
-    const int64_t c = (total + wgs - 1) / wgs;
-    return (c + wk - 1) / wk * wk;
+// Workgroups of a launch: two of four waves per compute unit.
+constexpr int kWgs = 512;
+
+// Steps per workgroup, a multiple of the waves along the tokens (a power of two).
+__device__ __forceinline__ int64_t share(int64_t total, int wk) {
+    const int64_t c = (total + kWgs - 1) / kWgs;
+    return (c + wk - 1) & ~(int64_t)(wk - 1);
 }
 
 // Eight dimensions (tokens) of a packet as halves.
@@ -164,8 +168,21 @@ __device__ __forceinline__ half8 packet_half(const uint4 &p, int hf) {
     else return __builtin_bit_cast(half8, p);
 }
 
-__device__ __forceinline__ bool finite_half(_Float16 h) {
-    return (__builtin_bit_cast(uint16_t, h) & 0x7C00u) != 0x7C00u;
+// Nonzero where one of a word's elements (2 fp16, 4 fp8) is not finite.
+template <bool FP8>
+__device__ __forceinline__ uint32_t odd_bits(uint32_t w) {
+    if constexpr (FP8)  // 0x7F or 0xFF: adding 1 to the low seven bits carries into the eighth
+        return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    else  // exponent all ones: adding one step of it carries into the sign's place
+        return ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+}
+
+// The word with those elements zero.
+template <bool FP8>
+__device__ __forceinline__ uint32_t drop_odd(uint32_t w) {
+    const uint32_t b = odd_bits<FP8>(w);
+    if constexpr (FP8) return w & ~((b >> 7) * 0xFFu);
+    else return w & ~((b >> 15) * 0xFFFFu);
 }
 
 __device__ __forceinline__ float over_groups_max(float v) {
@@ -198,12 +215,17 @@ struct Cfg {
     static constexpr bool HALF = MODE == kHalf;
     static constexpr bool SPLIT = !Q16;            // hi + lo
     static constexpr bool LO = SPLIT && !HALF;     // lo takes instructions of its own
+    static constexpr int PL = LO ? 2 : 1;          // planes of queries
+    static constexpr bool QLDS = MODE == kTwo;     // queries in LDS, to leave registers
+    static constexpr int QBYTES = QLDS ? 4 * PL * NQ * KS * 1024 : 0;
     static constexpr int COLS = HALF ? 8 : 16 * NQ;  // columns per wave
     static constexpr int PITCH = D + 4;
+    // waves per SIMD the registers have to leave room for
+    static constexpr int WAVES = D > 128 ? 1 : MODE == kTwo ? 2 : D > 64 ? 2 : 3;
 };
 
 template <bool FP8, bool Q16, int D, int MODE>
-__global__ __launch_bounds__(kThreads) void attend_kernel(Args a) {
+__global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void attend_kernel(Args a) {
     using C = Cfg<FP8, Q16, D, MODE>;
     constexpr int E = C::E, TS = C::TS, TT = C::TT, HF = C::HF, KP = C::KP, DT = C::DT, NQ = C::NQ;
     constexpr uint32_t kAll = (1u << E) - 1u;
@@ -217,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(Args a) {
 
     int64_t incl0 = 0, base;
     const int64_t total = plan_total<TS>(a, cw, lane, incl0);
-    const int64_t per = share(total, gridDim.x, WK);
+    const int64_t per = share(total, WK);
     int64_t p = (int64_t)blockIdx.x * per;
     const int64_t end = p + per < total ? p + per : total;
     if (p >= end) return;
@@ -238,7 +260,16 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(Args a) {
         const int32_t *trow = a.table + (size_t)r * a.width;
 
         // ---- queries as B operands ----
-        half8 qh[NQ][C::KS], ql[C::LO ? NQ : 1][C::LO ? C::KS : 1];
+        half8 qr[C::QLDS ? 1 : C::PL][C::QLDS ? 1 : NQ][C::QLDS ? 1 : C::KS];
+        half8 *qs = reinterpret_cast<half8 *>(lds) + (size_t)wv * (C::QBYTES / 64) + lane;
+        auto q_put = [&](int p, int j, int i, const half8 &x) {
+            if constexpr (C::QLDS) qs[((p * NQ + j) * C::KS + i) * 64] = x;
+            else qr[p][j][i] = x;
+        };
+        auto q_get = [&](int p, int j, int i) {
+            if constexpr (C::QLDS) return qs[((p * NQ + j) * C::KS + i) * 64];
+            else return qr[p][j][i];
+        };
         float cf[NQ];
         uint64_t bits[NQ];
 #pragma unroll
@@ -262,7 +293,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(Args a) {
                     const int d = ((i / HF) * 4 + g) * E + (i % HF) * 8;
                     half8 x = {0, 0, 0, 0, 0, 0, 0, 0};
                     if (real && d < D) x = *reinterpret_cast<const half8 *>(qp + d);
-                    qh[j][i] = x;
+                    q_put(0, j, i, x);
                 }
                 cf[j] = unit_scale;
             } else {
@@ -302,10 +333,10 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(Args a) {
                         lo[e] = (_Float16)(v - (float)hi[e]);
                     }
                     if constexpr (C::HALF) {
-                        qh[j][i] = n < 8 ? hi : lo;
+                        q_put(0, j, i, n < 8 ? hi : lo);
                     } else {
-                        qh[j][i] = hi;
-                        ql[j][i] = lo;
+                        q_put(0, j, i, hi);
+                        q_put(1, j, i, lo);
                     }
                 }
             }
@@ -323,73 +354,103 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(Args a) {
             for (int d = 0; d < DT; ++d) o[j][d] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
 
-        for (int st = s0 + wk; st < s1; st += WK) {
-            const int t0 = st * TS;
-            // a lane's key packets belong to token group n / 4, its value packets to group g
-            const int tk = t0 + (n >> 2) * E, tv = t0 + g * E;
-            int pk = tk < rq.tot ? trow[tk >> a.shift] : -1;
-            int pv = tv < rq.tot ? trow[tv >> a.shift] : -1;
-            const bool bad = pk < 0 || pk >= a.pages || pv < 0 || pv >= a.pages;
-            const bool masked = t0 + TS > rq.L || __any(bad);
-            const bool ok_v = pv >= 0 && pv < a.pages;
-            if (pk < 0 || pk >= a.pages) pk = 0;
-            if (!ok_v) pv = 0;
-
-            uint4 kp[TT][KP], vp[DT];
-            {
-                const u32x4_t *kb = reinterpret_cast<const u32x4_t *>(a.k) +
-                                    ((size_t)pk * a.H + h) * ((size_t)C::NPK << a.shift);
-                const int o0 = (tk & (ps - 1)) + (n & 3);
+        // ---- the steps of this wave.  Keys of the next step are requested as soon as this
+        // step's scores are taken, its values as soon as this step's have been used, its page
+        // numbers a step earlier still: every load has half a step or more to arrive.
+        const int tkl = (n >> 2) * E, tvl = g * E;  // first token of a lane's key, value packets
+        const u32x4_t *kbase = reinterpret_cast<const u32x4_t *>(a.k) +
+                               (size_t)h * ((size_t)C::NPK << a.shift) + ((size_t)g << a.shift) + (n & 3);
+        const u32x4_t *vbase =
+            reinterpret_cast<const u32x4_t *>(a.v) + (size_t)h * (ps / E) * D + n;
+        const size_t kstride = (size_t)a.H * ((size_t)C::NPK << a.shift);  // packets per page
+        const size_t vstride = (size_t)a.H * (ps / E) * D;
+        u32x4_t kp[TT][KP], vp[DT];
+        auto pages_of = [&](int st, int &pk, int &pv) {
+            const int tk = st * TS + tkl, tv = st * TS + tvl;
+            pk = st < s1 && tk < rq.tot ? trow[tk >> a.shift] : -1;
+            pv = st < s1 && tv < rq.tot ? trow[tv >> a.shift] : -1;
+        };
+        auto there = [&](int pg) { return (uint32_t)pg < (uint32_t)a.pages; };
+        auto load_k = [&](int st, int pk) {  // a page that is not there reads page 0 (and is masked)
+            const u32x4_t *kb = kbase + (size_t)(there(pk) ? pk : 0) * kstride +
+                                ((st * TS + tkl) & (ps - 1));
 #pragma unroll
-                for (int t = 0; t < TT; ++t)
+            for (int i = 0; i < KP; ++i) {
+                const bool real = C::NPK % 4 == 0 || i * 4 + g < C::NPK;
 #pragma unroll
-                    for (int i = 0; i < KP; ++i) {
-                        const int pkt = i * 4 + g;
-                        u32x4_t x = {0u, 0u, 0u, 0u};
-                        if (C::NPK % 4 == 0 || pkt < C::NPK)
-                            x = kb[((size_t)pkt << a.shift) + o0 + 4 * t];
-                        kp[t][i] = __builtin_bit_cast(uint4, x);
-                    }
-                const u32x4_t *vb = reinterpret_cast<const u32x4_t *>(a.v) +
-                                    (((size_t)pv * a.H + h) * (ps / E) + (tv & (ps - 1)) / E) * D + n;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) vp[d] = __builtin_bit_cast(uint4, vb[d * 16]);
+                for (int t = 0; t < TT; ++t) {
+                    kp[t][i] = u32x4_t{0u, 0u, 0u, 0u};
+                    if (real) kp[t][i] = kb[((size_t)(i * 4) << a.shift) + 4 * t];
+                }
             }
+        };
+        auto load_v = [&](int st, int pv) {
+            const u32x4_t *vb = vbase + (size_t)(there(pv) ? pv : 0) * vstride +
+                                (size_t)((((st * TS + tvl) & (ps - 1)) / E) * D);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) vp[d] = vb[d * 16];
+        };
+        int st = s0 + wk;
+        int pk0, pv0, pk1, pv1;  // pages of this step and the next
+        pages_of(st, pk0, pv0);
+        pages_of(st + WK, pk1, pv1);
+        if (st < s1) {
+            load_k(st, pk0);
+            load_v(st, pv0);
+        }
+        for (; st < s1; st += WK) {
+            const int t0 = st * TS, tv = t0 + tvl;
+            const bool ok_v = there(pv0);
+            const bool masked = t0 + TS > rq.L || __any(!ok_v || !there(pk0));
+            int pk2, pv2;
+            pages_of(st + 2 * WK, pk2, pv2);
 
-            // ---- scores ----
+            // ---- scores, in units of log2 ----
             f32x4 s[NQ][TT];
 #pragma unroll
             for (int t = 0; t < TT; ++t)
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) s[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int t = 0; t < TT; ++t)
+            for (int i = 0; i < C::KS; ++i) {
+                // queries from LDS: no more than two instructions' worth at a time
+                if (C::QLDS && i % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+                half8 qx[NQ], qy[NQ];
 #pragma unroll
-                for (int i = 0; i < C::KS; ++i) {
-                    const half8 kx = packet_half<FP8>(kp[t][i / HF], i % HF);
+                for (int j = 0; j < NQ; ++j) {
+                    qx[j] = q_get(0, j, i);
+                    if constexpr (C::LO) qy[j] = q_get(1, j, i);
+                }
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    const half8 kx = packet_half<FP8>(__builtin_bit_cast(uint4, kp[t][i / HF]), i % HF);
 #pragma unroll
                     for (int j = 0; j < NQ; ++j) {
-                        s[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kx, qh[j][i], s[j][t], 0, 0, 0);
+                        s[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kx, qx[j], s[j][t], 0, 0, 0);
                         if constexpr (C::LO)
-                            s[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kx, ql[j][i], s[j][t], 0, 0, 0);
+                            s[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kx, qy[j], s[j][t], 0, 0, 0);
                     }
                 }
-            if constexpr (C::HALF) {
-                // columns n and n + 8 hold the products with hi and lo: add them
+            }
+            if (st + WK < s1) load_k(st + WK, pk1);
+#pragma unroll
+            for (int j = 0; j < NQ; ++j)
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int x = __float_as_int(s[0][t][i]);
-                        s[0][t][i] += __int_as_float(
-                            __builtin_amdgcn_update_dpp(0, x, 0x128, 0xF, 0xF, false));  // row_ror:8
+                        float x = s[j][t][i];
+                        if constexpr (C::HALF)  // columns n and n + 8 hold the products with hi and lo
+                            x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x128, 0xF,
+                                                                         0xF, true));  // row_ror:8
+                        s[j][t][i] = x * cf[j];
                     }
-            }
 
             // ---- masks: a lane's scores are the E consecutive tokens from tv on ----
             uint32_t hid[NQ];  // bit e: token tv + e does not count for this column
 #pragma unroll
             for (int j = 0; j < NQ; ++j) hid[j] = 0;
+            bool odd = false;  // some value of this step is not finite
             if (masked) {
                 const int jt = tv - rq.L;  // tv's place among the step's own tokens
                 const uint32_t old = jt >= 0 ? 0u : jt <= -E ? kAll : (1u << -jt) - 1u;
@@ -398,22 +459,48 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(Args a) {
                     const uint64_t own = jt >= 64 || jt <= -E ? 0ull
                                          : jt >= 0 ? bits[j] >> jt : bits[j] << -jt;
                     hid[j] = ok_v ? ~(old | (uint32_t)own) & kAll : kAll;
+#pragma unroll
+                    for (int t = 0; t < TT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if ((hid[j] >> (4 * t + i)) & 1) s[j][t][i] = kNegInf;
+                }
+                // values behind the last token or on no page are whatever memory holds: out
+                const int left = ok_v ? rq.tot - tv : 0;
+                uint32_t keep[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int n_in = left - w * (E / 4);  // tokens of this word that are there
+                    keep[w] = n_in >= E / 4 ? ~0u : n_in <= 0 ? 0u : (1u << (n_in * (128 / E))) - 1u;
+                }
+                uint32_t worst = 0;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        vp[d][w] &= keep[w];
+                        worst |= odd_bits<FP8>(vp[d][w]);
+                    }
+                odd = __any(worst != 0);
+                if (odd) {
+                    // values that are not finite leave the product too (a weight of 0 would
+                    // make NaN of them) and are added at the end
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) vp[d][w] = drop_odd<FP8>(vp[d][w]);
                 }
             }
 
             // ---- softmax weights ----
             half8 ph[NQ][HF], pl[C::LO ? NQ : 1][HF];
-            float pf[NQ][TT][4];
 #pragma unroll
             for (int j = 0; j < NQ; ++j) {
-                float top = kNegInf;
+                float top = s[j][0][0];
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x = s[j][t][i] * cf[j];
-                        top = fmaxf(top, ((hid[j] >> (4 * t + i)) & 1) ? kNegInf : x);
-                    }
+                    for (int i = 0; i < 4; ++i) top = fmaxf(top, s[j][t][i]);
                 if (__any(top > ref[j] + 8.0f)) {
                     const float up = fmaxf(ref[j], over_groups_max(top));
                     const float alpha = up == kNegInf ? 1.0f : exp2f(ref[j] - up);
@@ -425,20 +512,14 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(Args a) {
                 seen[j] = seen[j] || hid[j] != kAll;
                 const float sub = 6.0f - (ref[j] == kNegInf ? 0.0f : ref[j]);
 #pragma unroll
-                for (int t = 0; t < TT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float w = __builtin_amdgcn_exp2f(fmaf(s[j][t][i], cf[j], sub));
-                        if ((hid[j] >> (4 * t + i)) & 1) w = 0.0f;
-                        pf[j][t][i] = w;
-                        l[j] += w;
-                    }
-#pragma unroll
                 for (int hf = 0; hf < HF; ++hf)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float w = pf[j][2 * hf + e / 4][e % 4];
+                        const float w =
+                            __builtin_amdgcn_exp2f(s[j][2 * hf + e / 4][e % 4] + sub);
                         const _Float16 hi = (_Float16)w;
+                        if constexpr (Q16) l[j] += (float)hi;  // the weights as they are used
+                        else l[j] += w;
                         if constexpr (C::HALF) {
                             const _Float16 lo = (_Float16)(w - (float)hi);
                             ph[j][hf][e] = n < 8 ? hi : lo;
@@ -450,33 +531,11 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(Args a) {
             }
 
             // ---- outputs ----
-            bool odd = false;  // some value of this step is not finite
-            if (masked) {
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    half8 x[HF];
-#pragma unroll
-                    for (int hf = 0; hf < HF; ++hf) {
-                        x[hf] = packet_half<FP8>(vp[d], hf);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            odd = odd || (ok_v && tv + 8 * hf + e < rq.tot && !finite_half(x[hf][e]));
-                    }
-                }
-                odd = __any(odd);
-            }
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
                 for (int hf = 0; hf < HF; ++hf) {
-                    half8 vx = packet_half<FP8>(vp[d], hf);
-                    if (masked) {
-                        // tokens without a key, and values that are not finite, leave the product
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (!ok_v || tv + 8 * hf + e >= rq.tot || !finite_half(vx[e]))
-                                vx[e] = (_Float16)0.0f;
-                    }
+                    const half8 vx = packet_half<FP8>(__builtin_bit_cast(uint4, vp[d]), hf);
 #pragma unroll
                     for (int j = 0; j < NQ; ++j) {
                         o[j][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vx, ph[j][hf], o[j][d], 0, 0, 0);
@@ -484,24 +543,21 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(Args a) {
                             o[j][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vx, pl[j][hf], o[j][d], 0, 0, 0);
                     }
                 }
+            if (st + WK < s1) load_v(st + WK, pv1);
             if (odd) {
-                // Rare: add the values that are not finite one by one, to the columns that see
-                // them only (in the product a weight of 0 would still have made NaN of them).
-                for (int tok = 0; tok < TS; ++tok) {
+                // rare: the values that are not finite, one by one, for the columns that see them
+                for (int tok = 0; tok < TS && t0 + tok < rq.tot; ++tok) {
                     const int gs = tok / E, e = tok % E;
-                    if (t0 + tok >= rq.tot) break;
                     const int pg = trow[(t0 + tok) >> a.shift];
-                    if (pg < 0 || pg >= a.pages) continue;
+                    if (!there(pg)) continue;
                     const size_t row = ((size_t)pg * a.H + h) * (ps / E) + ((t0 + tok) & (ps - 1)) / E;
 #pragma unroll
                     for (int j = 0; j < NQ; ++j) {
-                        float w = 0.0f;
+                        float w = 0.0f;  // the weight's hi half: its sign and size are enough here
 #pragma unroll
-                        for (int t = 0; t < TT; ++t)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (4 * t + i == e) w = pf[j][t][i];
-                        w = __shfl(w, gs * 16 + n, 64);
+                        for (int x = 0; x < E; ++x)
+                            if (x == e) w = (float)ph[j][x / 8][x % 8];
+                        w = __shfl(w, gs * 16 + (C::HALF ? n & 7 : n), 64);
                         const bool on = !((__shfl((int)hid[j], gs * 16 + n, 64) >> e) & 1);
 #pragma unroll
                         for (int d = 0; d < DT; ++d)
@@ -517,6 +573,10 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(Args a) {
                     }
                 }
             }
+            pk0 = pk1;
+            pv0 = pv1;
+            pk1 = pk2;
+            pv1 = pv2;
         }
 
         // ---- the workgroup's share of the unit ----
@@ -538,6 +598,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(Args a) {
             }
         }
         // LDS: [wave][column][D + 4], then maxima and sums [wave][column][2]
+        if constexpr (C::QLDS) __syncthreads();  // every wave is done with its queries there
         float *lo_ = lds + (size_t)wv * C::COLS * C::PITCH;
         float *ml = lds + (size_t)4 * C::COLS * C::PITCH;
         if (!C::HALF || n < 8) {
@@ -614,17 +675,36 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(Args a) {
 
 // Joins the slots of the unit that workgroup blockIdx.x of the attention
 // launch began and did not finish: slot 2w + 1 holds its first part, the
-// following workgroups' slots 2w' the rest.  One thread per four outputs of a
-// column, the parts added in order.
+// following workgroups' slots 2w' the rest.  A thread takes four outputs of a
+// column and every JP-th part, four parts at a time so that their loads are in
+// flight together; the JP sums of a column are then added in order.
+constexpr int kJoinParts = 4;
+
+struct Sum {
+    float m, l;
+    f32x4 o;
+};
+
+__device__ __forceinline__ void join(Sum &a, float m, float l, const f32x4 &o) {
+    const float top = fmaxf(a.m, m);
+    const float f0 = top == kNegInf ? 1.0f : exp2f(a.m - top);
+    const float f1 = top == kNegInf ? 1.0f : exp2f(m - top);
+    a.l = f0 * a.l + f1 * l;
+    a.o = a.o * f0 + o * f1;
+    a.m = top;
+}
+
 template <bool FP8, bool Q16, int D, int MODE>
-__global__ __launch_bounds__(kThreads) void attend_join_kernel(Args a, int wgs) {
+__global__ __launch_bounds__(kThreads) void attend_join_kernel(Args a) {
     using C = Cfg<FP8, Q16, D, MODE>;
-    constexpr int TS = C::TS;
+    constexpr int TS = C::TS, JP = kJoinParts, TC = D / 4;  // threads per column and part group
+    constexpr int JC = kThreads / (TC * JP) < 1 ? 1 : kThreads / (TC * JP);  // columns per workgroup
+    __shared__ Sum part[JP][JC][TC];
     const int lane = threadIdx.x & 63;
     const int WK = 4 / a.wq, cw = C::COLS * a.wq;
     int64_t incl0 = 0, base;
     const int64_t total = plan_total<TS>(a, cw, lane, incl0);
-    const int64_t per = share(total, wgs, WK);
+    const int64_t per = share(total, WK);
     const int w = blockIdx.x;
     const int64_t p0 = (int64_t)w * per, end = p0 + per;
     if (end >= total) return;  // the last workgroup with work finishes its units
@@ -633,76 +713,88 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(Args a, int wgs) 
     const uint32_t unit = (uint32_t)(end - 1 - base) / (uint32_t)rq.steps;
     const int64_t u0 = base + (int64_t)unit * rq.steps, u1 = u0 + rq.steps;
     if (u0 < p0 || u1 <= end) return;  // begun earlier, or finished here
-    const int last = (int)((u1 - 1) / per);
+    // further workgroups that share the unit (u1 - end < steps fits 32 bits)
+    const uint32_t rest = (uint32_t)(u1 - end);
+    const int more = per >= rest ? 1 : (int)((rest + (uint32_t)per - 1) / (uint32_t)per);
     const int h = (int)(unit / (uint32_t)rq.nqt), qt = (int)(unit - (uint32_t)h * rq.nqt);
-    const int x = blockIdx.y * kThreads + threadIdx.x;
-    const int c = x / (D / 4), d4 = x - c * (D / 4);
-    const int cg = qt * cw + c;
-    if (c >= cw || cg >= rq.T * a.G) return;
-    float m = kNegInf, sum = 0.0f;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int i = w; i <= last; ++i) {
-        const size_t at = (size_t)(2 * i + (i == w ? 1 : 0)) * cw + c;
-        const float mx = a.part_ml[at * 2], lx = a.part_ml[at * 2 + 1];
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(a.part_o + at * D + d4 * 4);
-        const float top = fmaxf(m, mx);
-        const float f0 = top == kNegInf ? 1.0f : m == kNegInf ? 0.0f : exp2f(m - top);
-        const float f1 = top == kNegInf ? 1.0f : mx == kNegInf ? 0.0f : exp2f(mx - top);
-        sum = f0 * sum + f1 * lx;
-        acc = acc * f0 + v * f1;
-        m = top;
+    const int d4 = threadIdx.x % TC, jc = (threadIdx.x / TC) % JC, jp = threadIdx.x / (TC * JC);
+    const int c = blockIdx.y * JC + jc, cg = qt * cw + c;
+    const bool real = c < cw && cg < rq.T * a.G && jp < JP;
+    Sum acc{kNegInf, 0.0f, f32x4{0.f, 0.f, 0.f, 0.f}};
+    if (real) {
+        for (int i = jp; i <= more; i += 4 * JP) {
+            float m[4], l[4];
+            f32x4 o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int x = i + k * JP <= more ? i + k * JP : i;
+                const size_t at = (size_t)(2 * (w + x) + (x == 0 ? 1 : 0)) * cw + c;
+                m[k] = a.part_ml[at * 2];
+                l[k] = a.part_ml[at * 2 + 1];
+                o[k] = *reinterpret_cast<const f32x4 *>(a.part_o + at * D + d4 * 4);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k * JP <= more) join(acc, m[k], l[k], o[k]);
+        }
+        part[jp][jc][d4] = acc;
     }
-    const float inv = (FP8 ? a.vs[h] : 1.0f) / sum;
+    __syncthreads();
+    if (!real || jp != 0) return;
+    const int parts = more + 1 < JP ? more + 1 : JP;
+    for (int k = 1; k < parts; ++k) join(acc, part[k][jc][d4].m, part[k][jc][d4].l, part[k][jc][d4].o);
+    const float inv = (FP8 ? a.vs[h] : 1.0f) / acc.l;
     const int t = cg / a.G, gq = cg - t * a.G;
     const size_t at = (size_t)(rq.a0 + t) * a.ldo + (size_t)(h * a.G + gq) * D + d4 * 4;
     if constexpr (Q16) {
         half4 y;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = (_Float16)finish(acc[i], m, sum, inv);
+        for (int i = 0; i < 4; ++i) y[i] = (_Float16)finish(acc.o[i], acc.m, acc.l, inv);
         *reinterpret_cast<half4 *>(static_cast<_Float16 *>(a.out) + at) = y;
     } else {
         f32x4 y;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = finish(acc[i], m, sum, inv);
+        for (int i = 0; i < 4; ++i) y[i] = finish(acc.o[i], acc.m, acc.l, inv);
         *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = y;
     }
 }
 
 template <bool FP8, bool Q16, int D, int MODE>
-hipError_t launch_mode(const Args &a, int wgs, hipStream_t s) {
+hipError_t launch_mode(const Args &a, hipStream_t s) {
     using C = Cfg<FP8, Q16, D, MODE>;
     auto fn = attend_kernel<FP8, Q16, D, MODE>;
-    const size_t lds = (size_t)4 * C::COLS * (C::PITCH + 2) * 4;
+    size_t lds = (size_t)4 * C::COLS * (C::PITCH + 2) * 4;
+    if (lds < (size_t)C::QBYTES) lds = C::QBYTES;
     if (lds > 65536) {
         hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(fn),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess) return e;
     }
-    fn<<<wgs, kThreads, lds, s>>>(a);
+    fn<<<kWgs, kThreads, lds, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int threads = C::COLS * a.wq * (D / 4);
+    constexpr int jc = kThreads / (D / 4 * kJoinParts) < 1 ? 1 : kThreads / (D / 4 * kJoinParts);
     attend_join_kernel<FP8, Q16, D, MODE>
-        <<<dim3(wgs, (threads + kThreads - 1) / kThreads), kThreads, 0, s>>>(a, wgs);
+        <<<dim3(kWgs, (C::COLS * a.wq + jc - 1) / jc), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
 template <bool FP8, bool Q16, int D>
-hipError_t launch_dim(const Args &a, int mode, int wgs, hipStream_t s) {
+hipError_t launch_dim(const Args &a, int mode, hipStream_t s) {
     if constexpr (D <= 128)
-        if (mode == kTwo) return launch_mode<FP8, Q16, D, kTwo>(a, wgs, s);
+        if (mode == kTwo) return launch_mode<FP8, Q16, D, kTwo>(a, s);
     if constexpr (!Q16)
-        if (mode == kHalf) return launch_mode<FP8, Q16, D, kHalf>(a, wgs, s);
-    return launch_mode<FP8, Q16, D, kOne>(a, wgs, s);
+        if (mode == kHalf) return launch_mode<FP8, Q16, D, kHalf>(a, s);
+    return launch_mode<FP8, Q16, D, kOne>(a, s);
 }
 
 template <bool FP8, bool Q16>
-hipError_t launch_all(const Args &a, int dim, int mode, int wgs, hipStream_t s) {
+hipError_t launch_all(const Args &a, int dim, int mode, hipStream_t s) {
     switch (dim) {
-        case 64: return launch_dim<FP8, Q16, 64>(a, mode, wgs, s);
-        case 96: return launch_dim<FP8, Q16, 96>(a, mode, wgs, s);
-        case 128: return launch_dim<FP8, Q16, 128>(a, mode, wgs, s);
-        default: return launch_dim<FP8, Q16, 256>(a, mode, wgs, s);
+        case 64: return launch_dim<FP8, Q16, 64>(a, mode, s);
+        case 96: return launch_dim<FP8, Q16, 96>(a, mode, s);
+        case 128: return launch_dim<FP8, Q16, 128>(a, mode, s);
+        default: return launch_dim<FP8, Q16, 256>(a, mode, s);
     }
 }
 

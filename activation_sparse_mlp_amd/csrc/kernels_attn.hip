@@ -3,14 +3,10 @@
 
 namespace spffn {
 
-hipError_t launch_attend_f16(const attn::Args &a, bool q16, int dim, int mode, int wgs,
-                             hipStream_t s);
-hipError_t launch_attend_fp8(const attn::Args &a, bool q16, int dim, int mode, int wgs,
-                             hipStream_t s);
+hipError_t launch_attend_f16(const attn::Args &a, bool q16, int dim, int mode, hipStream_t s);
+hipError_t launch_attend_fp8(const attn::Args &a, bool q16, int dim, int mode, hipStream_t s);
 
 namespace {
-
-constexpr int kAttnWgs = 512;  // two workgroups of four waves per compute unit
 
 struct Shape {
     int mode, wq, cols;  // columns a workgroup takes at a time
@@ -34,7 +30,7 @@ Shape attn_shape(int G, int dim, int max_new, bool q16) {
 
 size_t attn_ws_bytes(int heads, int kv_heads, int dim, int max_new, bool q16) {
     const Shape sh = attn_shape(heads / kv_heads, dim, max_new, q16);
-    return (size_t)2 * kAttnWgs * sh.cols * (dim + 2) * 4;
+    return (size_t)2 * attn::kWgs * sh.cols * (dim + 2) * 4;
 }
 
 hipError_t launch_tree_attention(const KvCache &c, const AttnCall &q, void *ws, hipStream_t s) {
@@ -52,7 +48,7 @@ hipError_t launch_tree_attention(const KvCache &c, const AttnCall &q, void *ws, 
     a.table = q.table;
     a.mask = q.mask;
     a.part_o = static_cast<float *>(ws);
-    a.part_ml = a.part_o + (size_t)2 * kAttnWgs * sh.cols * c.D;
+    a.part_ml = a.part_o + (size_t)2 * attn::kWgs * sh.cols * c.D;
     a.ldq = q.ldq;
     a.ldo = q.ldo;
     a.scale = q.scale;
@@ -65,8 +61,8 @@ hipError_t launch_tree_attention(const KvCache &c, const AttnCall &q, void *ws, 
     a.shift = c.shift;
     a.max_new = q.max_new;
     a.wq = sh.wq;
-    return c.fp8 ? launch_attend_fp8(a, q.q16, c.D, sh.mode, kAttnWgs, s)
-                 : launch_attend_f16(a, q.q16, c.D, sh.mode, kAttnWgs, s);
+    return c.fp8 ? launch_attend_fp8(a, q.q16, c.D, sh.mode, s)
+                 : launch_attend_f16(a, q.q16, c.D, sh.mode, s);
 }
 
 }  // namespace spffn
