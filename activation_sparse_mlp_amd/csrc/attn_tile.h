@@ -22,10 +22,12 @@
 //   O^T += V^T P^T  A operand: 16 dimensions x 32 tokens, a lane's packet is 8
 //                 (16) tokens of one dimension.
 // The cache's packet layout makes both loads 256 contiguous bytes per 16 lanes,
-// straight into registers, with no transposition and no LDS.  Token rows of S^T
-// are taken in the order that leaves a lane's scores being exactly the tokens its
-// P^T operand needs (row 4g + i of tile t is token E g + 4t + i), so the softmax
-// weights go from one product to the next without leaving their lane.
+// whole cache lines straight into registers, with no transposition and no LDS.
+// (Token rows picked so that the weights came out of the first product where the
+// second wants them would read half lines, twice each: the cache then stalls on
+// its own misses, 0.63 us a request instead of 0.2.)  A lane's scores are tokens
+// 16 t + 4 g + i; the second product wants E g + e: a transposition of four-token
+// groups among the four rows of lanes, two lane swaps per register of weights.
 //
 // Precision.  fp32 queries are split in hi + lo halves after a power-of-two
 // scale per column, the softmax weights likewise (2^6 above the running
@@ -53,6 +55,12 @@ typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kThreads = 256;
 
+// Beginning and ending a unit costs a workgroup about as much time as this many
+// steps, so a unit counts for as many more when the work is dealt out (a share
+// that ends within them leaves the unit to the next workgroup).  Sixteen ragged
+// requests of 96 heads: 397 us with 0, 313 with 4, 287 with 8 and with 16.
+constexpr int kSetup = 8;
+
 enum Mode : int { kHalf = 0, kOne = 1, kTwo = 2 };  // columns per wave: 8, 16, 32
 
 struct Args {
@@ -71,12 +79,12 @@ struct Args {
 
 // What a request asks for: committed length L, tokens T, keys tot = L + T.
 struct Req {
-    int a0, L, T, tot, steps, nqt;
+    int a0, L, T, tot, steps, span, nqt;
 };
 
 template <int TS>
 __device__ __forceinline__ Req request(const Args &a, int r, int cw) {
-    Req q;
+    Req q;  // (r may differ between lanes)
     int a0 = a.starts[r], a1 = a.starts[r + 1];
     a0 = a0 < 0 ? 0 : a0;
     a1 = a1 > a.N ? a.N : a1;
@@ -91,6 +99,7 @@ __device__ __forceinline__ Req request(const Args &a, int r, int cw) {
     q.T = T;
     q.tot = cap - L < T ? cap : L + T;
     q.steps = (q.tot + TS - 1) / TS;
+    q.span = q.steps + kSetup;
     q.nqt = (T * a.G + cw - 1) / cw;
     return q;
 }
@@ -100,7 +109,7 @@ template <int TS>
 __device__ __forceinline__ int64_t req_steps(const Args &a, int r, int cw) {
     if (r >= a.R) return 0;
     const Req q = request<TS>(a, r, cw);
-    return (int64_t)q.steps * q.nqt * a.H;
+    return (int64_t)q.span * q.nqt * a.H;
 }
 
 __device__ __forceinline__ int64_t scan64(int64_t v, int lane) {
@@ -112,6 +121,18 @@ __device__ __forceinline__ int64_t scan64(int64_t v, int lane) {
     return v;
 }
 
+// A value that every lane holds, in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    return (int64_t)((uint64_t)(uint32_t)uniform((int)(uint32_t)v) |
+                     (uint64_t)(uint32_t)uniform((int)((uint64_t)v >> 32)) << 32);
+}
+
+__device__ __forceinline__ Req uniform(const Req &q) {
+    return Req{uniform(q.a0), uniform(q.L), uniform(q.T), uniform(q.tot), uniform(q.steps),
+               uniform(q.span), uniform(q.nqt)};
+}
+
 // Every wave computes the plan for itself: the total and each workgroup's share.
 template <int TS>
 __device__ __forceinline__ int64_t plan_total(const Args &a, int cw, int lane, int64_t &incl0) {
@@ -121,7 +142,7 @@ __device__ __forceinline__ int64_t plan_total(const Args &a, int cw, int lane, i
         if (b == 0) incl0 = incl;
         total += __shfl(incl, 63, 64);
     }
-    return total;
+    return uniform(total);
 }
 
 // The request that holds position p < total, and its first position.
@@ -135,8 +156,8 @@ __device__ __forceinline__ int plan_find(const Args &a, int cw, int lane, int64_
         const uint64_t past = __ballot(p < incl);
         if (past) {
             const int i = __ffsll((long long)past) - 1;
-            base = i ? __shfl(incl, i - 1, 64) : before;
-            return b + i;
+            base = uniform(i ? __shfl(incl, i - 1, 64) : before);
+            return uniform(b + i);
         }
         before = __shfl(incl, 63, 64);
     }
@@ -144,12 +165,12 @@ __device__ __forceinline__ int plan_find(const Args &a, int cw, int lane, int64_
     return 0;
 }
 
-// Workgroups of a launch: two of four waves per compute unit.
-constexpr int kWgs = 512;
+constexpr int kMaxWgs = 768;  // of a launch
 
 // Steps per workgroup, a multiple of the waves along the tokens (a power of two).
+template <int WGS>
 __device__ __forceinline__ int64_t share(int64_t total, int wk) {
-    const int64_t c = (total + kWgs - 1) / kWgs;
+    const int64_t c = (int64_t)((uint64_t)(total + WGS - 1) / (uint64_t)WGS);
     return (c + wk - 1) & ~(int64_t)(wk - 1);
 }
 
@@ -194,11 +215,47 @@ __device__ __forceinline__ float over_groups_sum(float v) {
     return v + __shfl_xor(v, 32, 64);
 }
 
+template <bool ONCE>
+__device__ __forceinline__ u32x4_t fetch(const uint8_t *p) {
+    if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(p));
+    else return *reinterpret_cast<const u32x4_t *>(p);
+}
+
 // Final value of one output element: o / l, 0 for a row that saw no key, NaN
 // for one whose every key scored -inf.
 __device__ __forceinline__ float finish(float o, float m, float l, float inv) {
     if (m == kNegInf) return l > 0.0f ? __builtin_nanf("") : l == 0.0f ? 0.0f : l;
     return o * inv;
+}
+
+// x's odd rows of 16 lanes with y's even rows; x's upper 32 lanes with y's lower.
+__device__ __forceinline__ void swap16(uint2 &x, uint2 &y) {
+    const auto a = __builtin_amdgcn_permlane16_swap(x.x, y.x, false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(x.y, y.y, false, false);
+    x = make_uint2(a[0], b[0]);
+    y = make_uint2(a[1], b[1]);
+}
+__device__ __forceinline__ void swap32(uint2 &x, uint2 &y) {
+    const auto a = __builtin_amdgcn_permlane32_swap(x.x, y.x, false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(x.y, y.y, false, false);
+    x = make_uint2(a[0], b[0]);
+    y = make_uint2(a[1], b[1]);
+}
+
+// Weights of tokens 16 t + 4 g + i (register t, lane row g) to the B operand's
+// tokens E g + e.
+__device__ __forceinline__ void to_packets(uint2 (&w)[2], half8 (&p)[1]) {
+    swap32(w[0], w[1]);
+    swap16(w[0], w[1]);
+    p[0] = __builtin_bit_cast(half8, make_uint4(w[0].x, w[0].y, w[1].x, w[1].y));
+}
+__device__ __forceinline__ void to_packets(uint2 (&w)[4], half8 (&p)[2]) {
+    swap32(w[0], w[2]);
+    swap32(w[1], w[3]);
+    swap16(w[0], w[1]);
+    swap16(w[2], w[3]);
+    p[0] = __builtin_bit_cast(half8, make_uint4(w[0].x, w[0].y, w[1].x, w[1].y));
+    p[1] = __builtin_bit_cast(half8, make_uint4(w[2].x, w[2].y, w[3].x, w[3].y));
 }
 
 template <bool FP8, bool Q16, int D, int MODE>
@@ -221,7 +278,10 @@ struct Cfg {
     static constexpr int COLS = HALF ? 8 : 16 * NQ;  // columns per wave
     static constexpr int PITCH = D + 4;
     // waves per SIMD the registers have to leave room for
-    static constexpr int WAVES = D > 128 ? 1 : MODE == kTwo ? 2 : D > 64 ? 2 : 3;
+    static constexpr int WAVES = D > 128 ? 1 : MODE == kTwo || D > 96 ? 2 : 3;
+    static constexpr int WGS = 256 * WAVES;  // workgroups of a launch: all resident at once
+    // a step's keys and values are read once by one wave: past the caches, then
+    static constexpr bool ONCE = MODE != kTwo;
 };
 
 template <bool FP8, bool Q16, int D, int MODE>
@@ -239,22 +299,23 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
 
     int64_t incl0 = 0, base;
     const int64_t total = plan_total<TS>(a, cw, lane, incl0);
-    const int64_t per = share(total, WK);
+    const int64_t per = share<C::WGS>(total, WK);
     int64_t p = (int64_t)blockIdx.x * per;
     const int64_t end = p + per < total ? p + per : total;
     if (p >= end) return;
     int r = plan_find<TS>(a, cw, lane, incl0, p, base);
-    r = __builtin_amdgcn_readfirstlane(r);
 
-    Req rq = request<TS>(a, r, cw);
-    int64_t rsteps = (int64_t)rq.steps * rq.nqt * a.H;
+    Req rq = uniform(request<TS>(a, r, cw));
+    int64_t rsteps = (int64_t)rq.span * rq.nqt * a.H;
     while (true) {
         // ---- the segment: steps [s0, s1) of unit (r, h, qt) ----
         const uint32_t rel = (uint32_t)(p - base);
-        const uint32_t unit = rel / (uint32_t)rq.steps;
-        const int s0 = (int)(rel - unit * (uint32_t)rq.steps);
-        const int s1 = end - p < rq.steps - s0 ? s0 + (int)(end - p) : rq.steps;
-        const int h = (int)(unit / (uint32_t)rq.nqt), qt = (int)(unit - (uint32_t)h * rq.nqt);
+        const uint32_t unit = (uint32_t)uniform((int)(rel / (uint32_t)rq.span));
+        const int x0 = (int)(rel - unit * (uint32_t)rq.span);  // its place in the unit's span
+        const int x1 = end - p < rq.span - x0 ? x0 + (int)(end - p) : rq.span;
+        if (x1 <= kSetup) break;  // the share's end: the unit is the next workgroup's
+        const int s0 = x0 > kSetup ? x0 - kSetup : 0, s1 = x1 - kSetup;
+        const int h = uniform((int)(unit / (uint32_t)rq.nqt)), qt = (int)(unit - (uint32_t)h * rq.nqt);
         const int n_cols = rq.T * a.G;
         const int col0 = (qt * WQ + wq) * C::COLS;
         const int32_t *trow = a.table + (size_t)r * a.width;
@@ -284,7 +345,10 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
                 const int tk = rq.tot - rq.L;
                 bits[j] &= tk <= 0 ? 0ull : (~0ull >> (64 - tk));
             }
-            const float unit_scale = a.scale * 1.44269504088896340736f * (FP8 ? a.ks[h] : 1.0f);
+            // scores are compared before they are scaled: the factor is kept positive
+            const float unit_scale =
+                fabsf(a.scale) * 1.44269504088896340736f * (FP8 ? fabsf(a.ks[h]) : 1.0f);
+            const bool flip = (a.scale < 0.0f) != (FP8 && a.ks[h] < 0.0f);
             const size_t at = (size_t)row * a.ldq + (size_t)(h * a.G + gq) * D;
             if constexpr (Q16) {
                 const _Float16 *qp = static_cast<const _Float16 *>(a.q) + at;
@@ -293,6 +357,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
                     const int d = ((i / HF) * 4 + g) * E + (i % HF) * 8;
                     half8 x = {0, 0, 0, 0, 0, 0, 0, 0};
                     if (real && d < D) x = *reinterpret_cast<const half8 *>(qp + d);
+                    if (flip) x = -x;
                     q_put(0, j, i, x);
                 }
                 cf[j] = unit_scale;
@@ -320,7 +385,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
                 odd = over_groups_sum(odd);
                 uint32_t eb = __float_as_uint(m) >> 23;
                 eb = eb < 16 ? 16 : eb > 254 ? 254 : eb;
-                const float up = __uint_as_float((267u - eb) << 23);  // largest in [2^13, 2^14)
+                const float up = __uint_as_float((267u - eb) << 23 | (flip ? 1u << 31 : 0u));  // to [2^13, 2^14)
                 // a query that is not finite makes every score NaN
                 cf[j] = unit_scale * __uint_as_float((eb - 13u) << 23) + odd;
 #pragma unroll
@@ -357,55 +422,66 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
         // ---- the steps of this wave.  Keys of the next step are requested as soon as this
         // step's scores are taken, its values as soon as this step's have been used, its page
         // numbers a step earlier still: every load has half a step or more to arrive.
-        const int tkl = (n >> 2) * E, tvl = g * E;  // first token of a lane's key, value packets
-        const u32x4_t *kbase = reinterpret_cast<const u32x4_t *>(a.k) +
-                               (size_t)h * ((size_t)C::NPK << a.shift) + ((size_t)g << a.shift) + (n & 3);
-        const u32x4_t *vbase =
-            reinterpret_cast<const u32x4_t *>(a.v) + (size_t)h * (ps / E) * D + n;
-        const size_t kstride = (size_t)a.H * ((size_t)C::NPK << a.shift);  // packets per page
-        const size_t vstride = (size_t)a.H * (ps / E) * D;
+        const int tvl = g * E;  // first token of a lane's value packet
+        const uint32_t klane = (((uint32_t)g << a.shift) + n) * 16;  // bytes within a tile's keys
+        const uint8_t *kbase = a.k + (size_t)h * ((size_t)C::NPK << a.shift) * 16;
+        const uint8_t *vbase = a.v + ((size_t)h * (ps / E) * D + n) * 16;
+        const uint64_t kstride = (uint64_t)a.H * ((size_t)C::NPK << a.shift) * 16;  // bytes per page
+        const uint64_t vstride = (uint64_t)a.H * (ps / E) * D * 16;
         u32x4_t kp[TT][KP], vp[DT];
-        auto pages_of = [&](int st, int &pk, int &pv) {
-            const int tk = st * TS + tkl, tv = st * TS + tvl;
-            pk = st < s1 && tk < rq.tot ? trow[tk >> a.shift] : -1;
-            pv = st < s1 && tv < rq.tot ? trow[tv >> a.shift] : -1;
+        // A step covers TT blocks of 16 tokens, each on one page: lane b (mod TT) holds block b's.
+        // No load here hangs on a condition: one that may be skipped would make the loads
+        // behind it be waited for as if it had been.  What is not wanted is read twice.
+        auto pages_of = [&](int st) {
+            const int tok = st * TS + 16 * (lane & (TT - 1));
+            const int pg = trow[(tok < rq.tot ? tok : rq.tot - 1) >> a.shift];
+            return tok < rq.tot ? pg : -1;
         };
+        auto next = [&](int st) { return st + WK < s1 ? st + WK : st; };
         auto there = [&](int pg) { return (uint32_t)pg < (uint32_t)a.pages; };
-        auto load_k = [&](int st, int pk) {  // a page that is not there reads page 0 (and is masked)
-            const u32x4_t *kb = kbase + (size_t)(there(pk) ? pk : 0) * kstride +
-                                ((st * TS + tkl) & (ps - 1));
+        auto load_k = [&](int st, int pgs) {  // a page that is not there reads page 0 (and is masked)
 #pragma unroll
-            for (int i = 0; i < KP; ++i) {
-                const bool real = C::NPK % 4 == 0 || i * 4 + g < C::NPK;
+            for (int t = 0; t < TT; ++t) {
+                const int pg = __builtin_amdgcn_readlane(pgs, t);
+                const uint8_t *kb = kbase + (uint64_t)(there(pg) ? pg : 0) * kstride +
+                                    (uint32_t)((st * TS + 16 * t) & (ps - 1)) * 16;
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    kp[t][i] = u32x4_t{0u, 0u, 0u, 0u};
-                    if (real) kp[t][i] = kb[((size_t)(i * 4) << a.shift) + 4 * t];
+                for (int i = 0; i < KP; ++i) {
+                    // a packet past the head's meets queries of 0: the lane's one before is as good
+                    const bool real = C::NPK % 4 == 0 || i * 4 + g < C::NPK;
+                    kp[t][i] =
+                        fetch<C::ONCE>(kb + ((uint32_t)((real ? i : i - 1) * 64) << a.shift) + klane);
                 }
             }
         };
-        auto load_v = [&](int st, int pv) {
-            const u32x4_t *vb = vbase + (size_t)(there(pv) ? pv : 0) * vstride +
-                                (size_t)((((st * TS + tvl) & (ps - 1)) / E) * D);
+        auto load_v = [&](int st, int pgs) {
+            uint64_t off = 0;
 #pragma unroll
-            for (int d = 0; d < DT; ++d) vp[d] = vb[d * 16];
+            for (int t = 0; t < TT; ++t) {
+                const int pg = __builtin_amdgcn_readlane(pgs, t);
+                const uint64_t x = (uint64_t)(there(pg) ? pg : 0) * vstride;
+                if (t == 0 || t == g * E / 16) off = x;
+            }
+            const uint8_t *vb =
+                vbase + off + (uint32_t)((((st * TS + tvl) & (ps - 1)) / E) * D) * 16;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) vp[d] = fetch<C::ONCE>(vb + d * 256);
         };
         int st = s0 + wk;
-        int pk0, pv0, pk1, pv1;  // pages of this step and the next
-        pages_of(st, pk0, pv0);
-        pages_of(st + WK, pk1, pv1);
-        if (st < s1) {
-            load_k(st, pk0);
-            load_v(st, pv0);
-        }
+        const int first = st < s1 ? st : s1 - 1;  // (a wave without a step reads and drops one)
+        int pg0 = pages_of(first), pg1 = pages_of(next(first));  // pages of this step and the next
+        __builtin_amdgcn_sched_barrier(0);  // in this order, or the loop waits for both at once
+        load_k(first, pg0);
+        __builtin_amdgcn_sched_barrier(0);
+        load_v(first, pg0);
+        __builtin_amdgcn_sched_barrier(0);
         for (; st < s1; st += WK) {
+            const int st1 = next(st);
             const int t0 = st * TS, tv = t0 + tvl;
-            const bool ok_v = there(pv0);
-            const bool masked = t0 + TS > rq.L || __any(!ok_v || !there(pk0));
-            int pk2, pv2;
-            pages_of(st + 2 * WK, pk2, pv2);
+            const bool masked = t0 + TS > rq.L || __any(!there(pg0));
+            const int pg2 = pages_of(next(st1));
 
-            // ---- scores, in units of log2 ----
+            // ---- scores (unscaled) ----
             f32x4 s[NQ][TT];
 #pragma unroll
             for (int t = 0; t < TT; ++t)
@@ -432,40 +508,44 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
                     }
                 }
             }
-            if (st + WK < s1) load_k(st + WK, pk1);
-#pragma unroll
-            for (int j = 0; j < NQ; ++j)
+            load_k(st1, pg1);
+            if constexpr (C::HALF) {
+                // columns n and n + 8 hold the products with hi and lo: add them
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x = s[j][t][i];
-                        if constexpr (C::HALF)  // columns n and n + 8 hold the products with hi and lo
-                            x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x128, 0xF,
-                                                                         0xF, true));  // row_ror:8
-                        s[j][t][i] = x * cf[j];
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        s[0][t][i] += __int_as_float(__builtin_amdgcn_mov_dpp(
+                            __float_as_int(s[0][t][i]), 0x128, 0xF, 0xF, true));  // row_ror:8
+            }
 
-            // ---- masks: a lane's scores are the E consecutive tokens from tv on ----
-            uint32_t hid[NQ];  // bit e: token tv + e does not count for this column
+            // ---- masks ----
+            uint32_t hid[NQ];  // bit 4t + i: token t0 + 16t + 4g + i does not count for this column
 #pragma unroll
             for (int j = 0; j < NQ; ++j) hid[j] = 0;
             bool odd = false;  // some value of this step is not finite
             if (masked) {
-                const int jt = tv - rq.L;  // tv's place among the step's own tokens
-                const uint32_t old = jt >= 0 ? 0u : jt <= -E ? kAll : (1u << -jt) - 1u;
 #pragma unroll
-                for (int j = 0; j < NQ; ++j) {
-                    const uint64_t own = jt >= 64 || jt <= -E ? 0ull
-                                         : jt >= 0 ? bits[j] >> jt : bits[j] << -jt;
-                    hid[j] = ok_v ? ~(old | (uint32_t)own) & kAll : kAll;
+                for (int t = 0; t < TT; ++t) {
+                    const int jt = t0 + 16 * t + 4 * g - rq.L;  // first one's place in the step's own
+                    const uint32_t old = jt >= 0 ? 0u : jt <= -4 ? 15u : (1u << -jt) - 1u;
+                    const bool on_page = there(__builtin_amdgcn_readlane(pg0, t));
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) {
+                        const uint64_t own = jt >= 64 || jt <= -4 ? 0ull
+                                             : jt >= 0 ? bits[j] >> jt : bits[j] << -jt;
+                        hid[j] |= (on_page ? ~(old | (uint32_t)own) & 15u : 15u) << (4 * t);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < NQ; ++j)
 #pragma unroll
                     for (int t = 0; t < TT; ++t)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             if ((hid[j] >> (4 * t + i)) & 1) s[j][t][i] = kNegInf;
-                }
                 // values behind the last token or on no page are whatever memory holds: out
+                const bool ok_v = there(__shfl(pg0, g * E / 16, 64));
                 const int left = ok_v ? rq.tot - tv : 0;
                 uint32_t keep[4];
 #pragma unroll
@@ -501,33 +581,61 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
                 for (int t = 0; t < TT; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) top = fmaxf(top, s[j][t][i]);
+                top *= cf[j];
                 if (__any(top > ref[j] + 8.0f)) {
                     const float up = fmaxf(ref[j], over_groups_max(top));
                     const float alpha = up == kNegInf ? 1.0f : exp2f(ref[j] - up);
                     l[j] *= alpha;
 #pragma unroll
-                    for (int d = 0; d < DT; ++d) o[j][d] *= alpha;
+                    for (int d = 0; d < DT; ++d) {
+                        __builtin_amdgcn_sched_barrier(0);  // a tile at a time: few registers
+                        o[j][d] *= alpha;
+                    }
                     ref[j] = up;
                 }
                 seen[j] = seen[j] || hid[j] != kAll;
                 const float sub = 6.0f - (ref[j] == kNegInf ? 0.0f : ref[j]);
 #pragma unroll
-                for (int hf = 0; hf < HF; ++hf)
+                for (int t = 0; t < TT; ++t)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float w =
-                            __builtin_amdgcn_exp2f(s[j][2 * hf + e / 4][e % 4] + sub);
-                        const _Float16 hi = (_Float16)w;
-                        if constexpr (Q16) l[j] += (float)hi;  // the weights as they are used
-                        else l[j] += w;
-                        if constexpr (C::HALF) {
-                            const _Float16 lo = (_Float16)(w - (float)hi);
-                            ph[j][hf][e] = n < 8 ? hi : lo;
-                        } else {
-                            ph[j][hf][e] = hi;
-                            if constexpr (C::LO) pl[j][hf][e] = (_Float16)(w - (float)hi);
+                    for (int i = 0; i < 4; ++i)
+                        s[j][t][i] = __builtin_amdgcn_exp2f(fmaf(s[j][t][i], cf[j], sub));
+                if (masked) {  // (a scale of 0 makes a hidden score NaN, not -inf)
+#pragma unroll
+                    for (int t = 0; t < TT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if ((hid[j] >> (4 * t + i)) & 1) s[j][t][i] = 0.0f;
+                }
+                uint2 wh[TT], wl[TT];  // four weights each
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    half4 hi, lo;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = s[j][t][i];
+                        hi[i] = (_Float16)w;
+                        if constexpr (!Q16) {
+                            lo[i] = (_Float16)(w - (float)hi[i]);
+                            l[j] += w;
                         }
+                        if constexpr (C::HALF) hi[i] = n < 8 ? hi[i] : lo[i];
                     }
+                    wh[t] = __builtin_bit_cast(uint2, hi);
+                    if constexpr (C::LO) wl[t] = __builtin_bit_cast(uint2, lo);
+                }
+                to_packets(wh, ph[j]);
+                if constexpr (C::LO) to_packets(wl, pl[j]);
+                if constexpr (Q16) {
+                    // the sum of the weights as they are used, by a product with ones
+                    f32x4 sum = {l[j], 0.f, 0.f, 0.f};
+                    const _Float16 one = (_Float16)1.0f;
+#pragma unroll
+                    for (int hf = 0; hf < HF; ++hf)
+                        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            half8{one, one, one, one, one, one, one, one}, ph[j][hf], sum, 0, 0, 0);
+                    l[j] = sum[0];
+                }
             }
 
             // ---- outputs ----
@@ -543,7 +651,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
                             o[j][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vx, pl[j][hf], o[j][d], 0, 0, 0);
                     }
                 }
-            if (st + WK < s1) load_v(st + WK, pv1);
+            load_v(st1, pg1);
             if (odd) {
                 // rare: the values that are not finite, one by one, for the columns that see them
                 for (int tok = 0; tok < TS && t0 + tok < rq.tot; ++tok) {
@@ -558,9 +666,11 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
                         for (int x = 0; x < E; ++x)
                             if (x == e) w = (float)ph[j][x / 8][x % 8];
                         w = __shfl(w, gs * 16 + (C::HALF ? n & 7 : n), 64);
-                        const bool on = !((__shfl((int)hid[j], gs * 16 + n, 64) >> e) & 1);
+                        const int hx = __shfl((int)hid[j], ((tok >> 2) & 3) * 16 + n, 64);
+                        const bool on = !((hx >> (4 * (tok >> 4) + (tok & 3))) & 1);
 #pragma unroll
-                        for (int d = 0; d < DT; ++d)
+                        for (int d = 0; d < DT; ++d) {
+                            __builtin_amdgcn_sched_barrier(0);  // few registers, not few cycles
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const size_t at = (row * D + d * 16 + 4 * g + i) * E + e;
@@ -570,13 +680,12 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
                                 else v = (float)reinterpret_cast<const _Float16 *>(a.v)[at];
                                 if (on && !(fabsf(v) < __builtin_inff())) o[j][d][i] += w * v;
                             }
+                        }
                     }
                 }
             }
-            pk0 = pk1;
-            pv0 = pv1;
-            pk1 = pk2;
-            pv1 = pv2;
+            pg0 = pg1;
+            pg1 = pg2;
         }
 
         // ---- the workgroup's share of the unit ----
@@ -584,7 +693,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
         float vs = FP8 ? a.vs[h] : 1.0f;
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            l[j] = over_groups_sum(l[j]);
+            if constexpr (!Q16) l[j] = over_groups_sum(l[j]);
             const bool any = __shfl_xor(seen[j], 16, 64) || seen[j];
             seen[j] = __shfl_xor(any, 32, 64) || any;
             if (ref[j] == kNegInf && l[j] == 0.0f) l[j] = seen[j] ? 1.0f : 0.0f;
@@ -659,15 +768,15 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
         }
 
         // ---- next segment ----
-        p += s1 - s0;
+        p += x1 - x0;
         if (p >= end) break;
         __syncthreads();  // the next segment reuses the LDS
         if (p - base >= rsteps) {
             do {
                 base += rsteps;
                 ++r;
-                rq = request<TS>(a, r, cw);
-                rsteps = (int64_t)rq.steps * rq.nqt * a.H;
+                rq = uniform(request<TS>(a, r, cw));
+                rsteps = (int64_t)rq.span * rq.nqt * a.H;
             } while (rsteps == 0);
         }
     }
@@ -704,16 +813,17 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(Args a) {
     const int WK = 4 / a.wq, cw = C::COLS * a.wq;
     int64_t incl0 = 0, base;
     const int64_t total = plan_total<TS>(a, cw, lane, incl0);
-    const int64_t per = share(total, WK);
+    const int64_t per = share<C::WGS>(total, WK);
     const int w = blockIdx.x;
     const int64_t p0 = (int64_t)w * per, end = p0 + per;
     if (end >= total) return;  // the last workgroup with work finishes its units
-    const int r = __builtin_amdgcn_readfirstlane(plan_find<TS>(a, cw, lane, incl0, end - 1, base));
-    const Req rq = request<TS>(a, r, cw);
-    const uint32_t unit = (uint32_t)(end - 1 - base) / (uint32_t)rq.steps;
-    const int64_t u0 = base + (int64_t)unit * rq.steps, u1 = u0 + rq.steps;
-    if (u0 < p0 || u1 <= end) return;  // begun earlier, or finished here
-    // further workgroups that share the unit (u1 - end < steps fits 32 bits)
+    const int r = plan_find<TS>(a, cw, lane, incl0, end - 1, base);
+    const Req rq = uniform(request<TS>(a, r, cw));
+    const uint32_t unit = (uint32_t)(end - 1 - base) / (uint32_t)rq.span;
+    const int64_t u0 = base + (int64_t)unit * rq.span, u1 = u0 + rq.span;
+    // begun earlier or later, or finished here
+    if (u0 + kSetup < p0 || u0 + kSetup >= end || u1 <= end) return;
+    // further workgroups that share the unit (u1 - end < span fits 32 bits)
     const uint32_t rest = (uint32_t)(u1 - end);
     const int more = per >= rest ? 1 : (int)((rest + (uint32_t)per - 1) / (uint32_t)per);
     const int h = (int)(unit / (uint32_t)rq.nqt), qt = (int)(unit - (uint32_t)h * rq.nqt);
@@ -770,12 +880,12 @@ hipError_t launch_mode(const Args &a, hipStream_t s) {
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess) return e;
     }
-    fn<<<kWgs, kThreads, lds, s>>>(a);
+    fn<<<C::WGS, kThreads, lds, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     constexpr int jc = kThreads / (D / 4 * kJoinParts) < 1 ? 1 : kThreads / (D / 4 * kJoinParts);
     attend_join_kernel<FP8, Q16, D, MODE>
-        <<<dim3(kWgs, (C::COLS * a.wq + jc - 1) / jc), kThreads, 0, s>>>(a);
+        <<<dim3(C::WGS, (C::COLS * a.wq + jc - 1) / jc), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
