@@ -63,6 +63,13 @@ constexpr int kSetup = 8;
 
 enum Mode : int { kHalf = 0, kOne = 1, kTwo = 2 };  // columns per wave: 8, 16, 32
 
+// What the second launch has to join for a workgroup of the first: the parts
+// of this many workgroups after it (0: nothing), of request tokens from a0 on.
+struct Task {
+    int more, a0, n_cols, h, qt;
+    int pad[3];
+};
+
 struct Args {
     const void *q;
     void *out;
@@ -71,6 +78,7 @@ struct Args {
     const int32_t *starts, *lens, *table;
     const int64_t *mask;
     float *part_o, *part_ml;
+    Task *tasks;
     int64_t ldq, ldo;
     float scale;
     int N, R, G, H, width, pages, shift, max_new;
@@ -228,6 +236,39 @@ __device__ __forceinline__ float finish(float o, float m, float l, float inv) {
     return o * inv;
 }
 
+struct Sum {
+    float m, l;
+    f32x4 o;
+};
+
+__device__ __forceinline__ void join(Sum &a, float m, float l, const f32x4 &o) {
+    const float top = fmaxf(a.m, m);
+    const float f0 = top == kNegInf ? 1.0f : exp2f(a.m - top);
+    const float f1 = top == kNegInf ? 1.0f : exp2f(m - top);
+    a.l = f0 * a.l + f1 * l;
+    a.o = a.o * f0 + o * f1;
+    a.m = top;
+}
+
+// Four dimensions, from `at` on, of column cg of kv head h.
+template <bool Q16, int D>
+__device__ __forceinline__ void store_out(const Args &a, int a0, int h, int cg, int at, const f32x4 &o,
+                                          float m, float l, float inv) {
+    const int t = cg / a.G, gq = cg - t * a.G;
+    const size_t to = (size_t)(a0 + t) * a.ldo + (size_t)(h * a.G + gq) * D + at;
+    if constexpr (Q16) {
+        half4 y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = (_Float16)finish(o[i], m, l, inv);
+        *reinterpret_cast<half4 *>(static_cast<_Float16 *>(a.out) + to) = y;
+    } else {
+        f32x4 y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = finish(o[i], m, l, inv);
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + to) = y;
+    }
+}
+
 // x's odd rows of 16 lanes with y's even rows; x's upper 32 lanes with y's lower.
 __device__ __forceinline__ void swap16(uint2 &x, uint2 &y) {
     const auto a = __builtin_amdgcn_permlane16_swap(x.x, y.x, false, false);
@@ -302,7 +343,11 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
     const int64_t per = share<C::WGS>(total, WK);
     int64_t p = (int64_t)blockIdx.x * per;
     const int64_t end = p + per < total ? p + per : total;
-    if (p >= end) return;
+    Task task{};
+    if (p >= end) {
+        if (threadIdx.x == 0) a.tasks[blockIdx.x] = task;
+        return;
+    }
     int r = plan_find<TS>(a, cw, lane, incl0, p, base);
 
     Req rq = uniform(request<TS>(a, r, cw));
@@ -706,66 +751,72 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
                             0, __float_as_int(o[j][d][i]), 0x128, 0xF, 0xF, false));
             }
         }
-        // LDS: [wave][column][D + 4], then maxima and sums [wave][column][2]
-        if constexpr (C::QLDS) __syncthreads();  // every wave is done with its queries there
-        float *lo_ = lds + (size_t)wv * C::COLS * C::PITCH;
-        float *ml = lds + (size_t)4 * C::COLS * C::PITCH;
-        if (!C::HALF || n < 8) {
+        const size_t slot = 2 * (size_t)blockIdx.x + (s0 == 0 ? 1 : 0);
+        if (!C::HALF && WK == 1) {
+            // every wave has whole columns: straight from the registers
 #pragma unroll
             for (int j = 0; j < NQ; ++j) {
-                const int c = j * 16 + n;
+                const int c = wq * C::COLS + j * 16 + n, cg = qt * cw + c;
+                if (cg < n_cols) {
+                    const float inv = vs / l[j];
 #pragma unroll
-                for (int d = 0; d < DT; ++d)
-                    *reinterpret_cast<f32x4 *>(lo_ + c * C::PITCH + d * 16 + 4 * g) = o[j][d];
-                if (g == 0) {
-                    ml[(wv * C::COLS + c) * 2] = ref[j];
-                    ml[(wv * C::COLS + c) * 2 + 1] = l[j];
+                    for (int d = 0; d < DT; ++d) {
+                        const int at = d * 16 + 4 * g;
+                        if (whole) store_out<Q16, D>(a, rq.a0, h, cg, at, o[j][d], ref[j], l[j], inv);
+                        else *reinterpret_cast<f32x4 *>(a.part_o + (slot * cw + c) * D + at) = o[j][d];
+                    }
+                    if (!whole && g == 0) {
+                        a.part_ml[(slot * cw + c) * 2] = ref[j];
+                        a.part_ml[(slot * cw + c) * 2 + 1] = l[j];
+                    }
                 }
             }
-        }
-        __syncthreads();
-        const size_t slot = 2 * (size_t)blockIdx.x + (s0 == 0 ? 1 : 0);
-        for (int x = threadIdx.x; x < cw * (D / 4); x += kThreads) {
-            const int c = x / (D / 4), d4 = x - c * (D / 4);
-            const int w0 = c / C::COLS, cc = c - w0 * C::COLS;  // wave along the columns, its column
-            const int cg = qt * cw + c;
-            if (cg >= n_cols) break;
-            float m = kNegInf;
-            for (int kx = 0; kx < WK; ++kx) m = fmaxf(m, ml[((kx * WQ + w0) * C::COLS + cc) * 2]);
-            float sum = 0.0f;
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-            for (int kx = 0; kx < WK; ++kx) {
-                const int wx = kx * WQ + w0;
-                const float mx = ml[(wx * C::COLS + cc) * 2];
-                const float f = m == kNegInf ? 1.0f : mx == kNegInf ? 0.0f : exp2f(mx - m);
-                const float lx = ml[(wx * C::COLS + cc) * 2 + 1];
-                sum += f * lx;
-                acc += f * *reinterpret_cast<const f32x4 *>(
-                               lds + ((size_t)wx * C::COLS + cc) * C::PITCH + d4 * 4);
-            }
-            if (whole) {
-                const float inv = vs / sum;
-                const int t = cg / a.G, gq = cg - t * a.G;
-                const size_t at = (size_t)(rq.a0 + t) * a.ldo + (size_t)(h * a.G + gq) * D + d4 * 4;
-                if constexpr (Q16) {
-                    half4 y;
+        } else {
+            // through LDS: [wave][column][D + 4], then maxima and sums [wave][column][2]
+            if constexpr (C::QLDS) __syncthreads();  // every wave is done with its queries there
+            float *lo_ = lds + (size_t)wv * C::COLS * C::PITCH;
+            float *ml = lds + (size_t)4 * C::COLS * C::PITCH;
+            if (!C::HALF || n < 8) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = (_Float16)finish(acc[i], m, sum, inv);
-                    *reinterpret_cast<half4 *>(static_cast<_Float16 *>(a.out) + at) = y;
+                for (int j = 0; j < NQ; ++j) {
+                    const int c = j * 16 + n;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+                        *reinterpret_cast<f32x4 *>(lo_ + c * C::PITCH + d * 16 + 4 * g) = o[j][d];
+                    if (g == 0) {
+                        ml[(wv * C::COLS + c) * 2] = ref[j];
+                        ml[(wv * C::COLS + c) * 2 + 1] = l[j];
+                    }
+                }
+            }
+            __syncthreads();
+            for (int x = threadIdx.x; x < cw * (D / 4); x += kThreads) {
+                const int c = x / (D / 4), d4 = x - c * (D / 4);
+                const int w0 = c / C::COLS, cc = c - w0 * C::COLS;  // wave along the columns, its column
+                const int cg = qt * cw + c;
+                if (cg >= n_cols) break;
+                Sum acc{kNegInf, 0.0f, f32x4{0.f, 0.f, 0.f, 0.f}};
+                for (int kx = 0; kx < WK; ++kx) {
+                    const int wx = kx * WQ + w0;
+                    const float *p_ml = ml + (wx * C::COLS + cc) * 2;
+                    join(acc, p_ml[0], p_ml[1],
+                         *reinterpret_cast<const f32x4 *>(
+                             lds + ((size_t)wx * C::COLS + cc) * C::PITCH + d4 * 4));
+                }
+                if (whole) {
+                    store_out<Q16, D>(a, rq.a0, h, cg, d4 * 4, acc.o, acc.m, acc.l, vs / acc.l);
                 } else {
-                    f32x4 y;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = finish(acc[i], m, sum, inv);
-                    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = y;
-                }
-            } else {
-                *reinterpret_cast<f32x4 *>(a.part_o + (slot * cw + c) * D + d4 * 4) = acc;
-                if (d4 == 0) {
-                    a.part_ml[(slot * cw + c) * 2] = m;
-                    a.part_ml[(slot * cw + c) * 2 + 1] = sum;
+                    *reinterpret_cast<f32x4 *>(a.part_o + (slot * cw + c) * D + d4 * 4) = acc.o;
+                    if (d4 == 0) {
+                        a.part_ml[(slot * cw + c) * 2] = acc.m;
+                        a.part_ml[(slot * cw + c) * 2 + 1] = acc.l;
+                    }
                 }
             }
         }
+        // a unit begun here and not finished: the workgroups after this one that go on with it
+        if (s0 == 0 && !whole)
+            task = Task{(int)((rq.span - x1 + per - 1) / per), rq.a0, n_cols, h, qt, {}};
 
         // ---- next segment ----
         p += x1 - x0;
@@ -780,92 +831,57 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
             } while (rsteps == 0);
         }
     }
+    if (threadIdx.x == 0) a.tasks[blockIdx.x] = task;
 }
 
 // Joins the slots of the unit that workgroup blockIdx.x of the attention
-// launch began and did not finish: slot 2w + 1 holds its first part, the
-// following workgroups' slots 2w' the rest.  A thread takes four outputs of a
-// column and every JP-th part, four parts at a time so that their loads are in
+// launch began and did not finish (its task): slot 2w + 1 holds the first part,
+// the following workgroups' slots 2w' the rest.  A thread takes four outputs of
+// a column and every JP-th part, four parts at a time so that their loads are in
 // flight together; the JP sums of a column are then added in order.
 constexpr int kJoinParts = 4;
+constexpr int kJoinRows = 16;  // workgroups that share a unit's columns, at most
 
-struct Sum {
-    float m, l;
-    f32x4 o;
-};
-
-__device__ __forceinline__ void join(Sum &a, float m, float l, const f32x4 &o) {
-    const float top = fmaxf(a.m, m);
-    const float f0 = top == kNegInf ? 1.0f : exp2f(a.m - top);
-    const float f1 = top == kNegInf ? 1.0f : exp2f(m - top);
-    a.l = f0 * a.l + f1 * l;
-    a.o = a.o * f0 + o * f1;
-    a.m = top;
-}
-
-template <bool FP8, bool Q16, int D, int MODE>
-__global__ __launch_bounds__(kThreads) void attend_join_kernel(Args a) {
-    using C = Cfg<FP8, Q16, D, MODE>;
-    constexpr int TS = C::TS, JP = kJoinParts, TC = D / 4;  // threads per column and part group
-    constexpr int JC = kThreads / (TC * JP) < 1 ? 1 : kThreads / (TC * JP);  // columns per workgroup
+template <bool FP8, bool Q16, int D>
+__global__ __launch_bounds__(kThreads) void attend_join_kernel(Args a, int cw) {
+    constexpr int JP = kJoinParts, TC = D / 4;  // threads per column and part group
+    constexpr int JC = kThreads / (TC * JP);    // columns at a time
     __shared__ Sum part[JP][JC][TC];
-    const int lane = threadIdx.x & 63;
-    const int WK = 4 / a.wq, cw = C::COLS * a.wq;
-    int64_t incl0 = 0, base;
-    const int64_t total = plan_total<TS>(a, cw, lane, incl0);
-    const int64_t per = share<C::WGS>(total, WK);
     const int w = blockIdx.x;
-    const int64_t p0 = (int64_t)w * per, end = p0 + per;
-    if (end >= total) return;  // the last workgroup with work finishes its units
-    const int r = plan_find<TS>(a, cw, lane, incl0, end - 1, base);
-    const Req rq = uniform(request<TS>(a, r, cw));
-    const uint32_t unit = (uint32_t)(end - 1 - base) / (uint32_t)rq.span;
-    const int64_t u0 = base + (int64_t)unit * rq.span, u1 = u0 + rq.span;
-    // begun earlier or later, or finished here
-    if (u0 + kSetup < p0 || u0 + kSetup >= end || u1 <= end) return;
-    // further workgroups that share the unit (u1 - end < span fits 32 bits)
-    const uint32_t rest = (uint32_t)(u1 - end);
-    const int more = per >= rest ? 1 : (int)((rest + (uint32_t)per - 1) / (uint32_t)per);
-    const int h = (int)(unit / (uint32_t)rq.nqt), qt = (int)(unit - (uint32_t)h * rq.nqt);
+    const Task task = a.tasks[w];
+    if (task.more == 0) return;
     const int d4 = threadIdx.x % TC, jc = (threadIdx.x / TC) % JC, jp = threadIdx.x / (TC * JC);
-    const int c = blockIdx.y * JC + jc, cg = qt * cw + c;
-    const bool real = c < cw && cg < rq.T * a.G && jp < JP;
-    Sum acc{kNegInf, 0.0f, f32x4{0.f, 0.f, 0.f, 0.f}};
-    if (real) {
-        for (int i = jp; i <= more; i += 4 * JP) {
-            float m[4], l[4];
-            f32x4 o[4];
+    for (int c0 = blockIdx.y * JC; c0 < cw; c0 += gridDim.y * JC) {
+        const int c = c0 + jc, cg = task.qt * cw + c;
+        const bool real = c < cw && cg < task.n_cols && jp < JP;  // (96 dimensions leave threads over)
+        Sum acc{kNegInf, 0.0f, f32x4{0.f, 0.f, 0.f, 0.f}};
+        if (real) {
+            for (int i = jp; i <= task.more; i += 4 * JP) {
+                float m[4], l[4];
+                f32x4 o[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int x = i + k * JP <= more ? i + k * JP : i;
-                const size_t at = (size_t)(2 * (w + x) + (x == 0 ? 1 : 0)) * cw + c;
-                m[k] = a.part_ml[at * 2];
-                l[k] = a.part_ml[at * 2 + 1];
-                o[k] = *reinterpret_cast<const f32x4 *>(a.part_o + at * D + d4 * 4);
+                for (int k = 0; k < 4; ++k) {
+                    const int x = i + k * JP <= task.more ? i + k * JP : i;
+                    const size_t at = (size_t)(2 * (w + x) + (x == 0 ? 1 : 0)) * cw + c;
+                    m[k] = a.part_ml[at * 2];
+                    l[k] = a.part_ml[at * 2 + 1];
+                    o[k] = *reinterpret_cast<const f32x4 *>(a.part_o + at * D + d4 * 4);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (i + k * JP <= task.more) join(acc, m[k], l[k], o[k]);
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (i + k * JP <= more) join(acc, m[k], l[k], o[k]);
+            part[jp][jc][d4] = acc;
         }
-        part[jp][jc][d4] = acc;
-    }
-    __syncthreads();
-    if (!real || jp != 0) return;
-    const int parts = more + 1 < JP ? more + 1 : JP;
-    for (int k = 1; k < parts; ++k) join(acc, part[k][jc][d4].m, part[k][jc][d4].l, part[k][jc][d4].o);
-    const float inv = (FP8 ? a.vs[h] : 1.0f) / acc.l;
-    const int t = cg / a.G, gq = cg - t * a.G;
-    const size_t at = (size_t)(rq.a0 + t) * a.ldo + (size_t)(h * a.G + gq) * D + d4 * 4;
-    if constexpr (Q16) {
-        half4 y;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = (_Float16)finish(acc.o[i], acc.m, acc.l, inv);
-        *reinterpret_cast<half4 *>(static_cast<_Float16 *>(a.out) + at) = y;
-    } else {
-        f32x4 y;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = finish(acc.o[i], acc.m, acc.l, inv);
-        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = y;
+        __syncthreads();
+        if (real && jp == 0) {
+            const int parts = task.more + 1 < JP ? task.more + 1 : JP;
+            for (int k = 1; k < parts; ++k)
+                join(acc, part[k][jc][d4].m, part[k][jc][d4].l, part[k][jc][d4].o);
+            store_out<Q16, D>(a, task.a0, task.h, cg, d4 * 4, acc.o, acc.m, acc.l,
+                              (FP8 ? a.vs[task.h] : 1.0f) / acc.l);
+        }
+        __syncthreads();
     }
 }
 
@@ -883,9 +899,10 @@ hipError_t launch_mode(const Args &a, hipStream_t s) {
     fn<<<C::WGS, kThreads, lds, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    constexpr int jc = kThreads / (D / 4 * kJoinParts) < 1 ? 1 : kThreads / (D / 4 * kJoinParts);
-    attend_join_kernel<FP8, Q16, D, MODE>
-        <<<dim3(C::WGS, (C::COLS * a.wq + jc - 1) / jc), kThreads, 0, s>>>(a);
+    constexpr int jc = kThreads / (D / 4 * kJoinParts);
+    const int cw = C::COLS * a.wq, rows = (cw + jc - 1) / jc;
+    attend_join_kernel<FP8, Q16, D>
+        <<<dim3(C::WGS, rows < kJoinRows ? rows : kJoinRows), kThreads, 0, s>>>(a, cw);
     return hipGetLastError();
 }
 

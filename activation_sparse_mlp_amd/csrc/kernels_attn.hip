@@ -30,7 +30,7 @@ Shape attn_shape(int G, int dim, int max_new, bool q16) {
 
 size_t attn_ws_bytes(int heads, int kv_heads, int dim, int max_new, bool q16) {
     const Shape sh = attn_shape(heads / kv_heads, dim, max_new, q16);
-    return (size_t)2 * attn::kMaxWgs * sh.cols * (dim + 2) * 4;
+    return (size_t)2 * attn::kMaxWgs * sh.cols * (dim + 2) * 4 + attn::kMaxWgs * sizeof(attn::Task);
 }
 
 hipError_t launch_tree_attention(const KvCache &c, const AttnCall &q, void *ws, hipStream_t s) {
@@ -49,6 +49,7 @@ hipError_t launch_tree_attention(const KvCache &c, const AttnCall &q, void *ws, 
     a.mask = q.mask;
     a.part_o = static_cast<float *>(ws);
     a.part_ml = a.part_o + (size_t)2 * attn::kMaxWgs * sh.cols * c.D;
+    a.tasks = reinterpret_cast<attn::Task *>(a.part_ml + (size_t)4 * attn::kMaxWgs * sh.cols);
     a.ldq = q.ldq;
     a.ldo = q.ldo;
     a.scale = q.scale;
