@@ -607,28 +607,53 @@ _ROW_DTYPES = {torch.float32: F32, torch.float16: F16}
 _CACHE_DTYPES = {torch.float16: F16, torch.float8_e4m3fn: FP8_E4M3}
 
 
-def _call(dev, name, *args):
-    """One entry point on the current stream of the tensors' device, which need
-    not be the current device."""
-    fn = getattr(load(), name)
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+# These calls take a few microseconds on the GPU, so the checks before them are
+# written to be cheap: one test per tensor that everything in order passes, and
+# the checks that say what is wrong only where it fails.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(index, name, *args):
+    """One entry point on the current stream of GPU `index`, which need not be
+    the current device."""
+    fn = getattr(_lib or load(), name)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
     if status != 0:
         _check(status, name)
 
 
-def _on(dev, **tensors):
-    """Raise ValueError unless every given tensor is on device dev."""
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+def _plain(t, dtype, n, index, name):
+    """A contiguous tensor of n elements of dtype on GPU `index`; its address."""
+    if t.__class__ is not torch.Tensor or t.dtype is not dtype or t.get_device() != index or \
+            t.numel() != n or not t.is_contiguous():
+        _dev(t, dtype, name, n)
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    return t.data_ptr()
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _maybe(t, dtype, n, index, name):
+    return None if t is None else _plain(t, dtype, n, index, name)
+
+
+def _work(ws, need, index):
+    """Address and bytes of a workspace tensor."""
+    nb = _ws_bytes(ws, need)
+    if ws.get_device() != index:
+        raise ValueError(f"ws is on {ws.device}, not on cuda:{index}")
+    return ws.data_ptr(), nb
+
+
+def _sizes(*checks):
+    """(tensor, elements, name) of every argument, before any of them is looked at closer."""
+    for t, n, name in checks:
+        if t is not None and t.numel() != n:
+            _size(t, n, name)
 
 
 class Q4Matrix:
@@ -656,8 +681,9 @@ class Q4Matrix:
         _dev(codes, torch.uint8, "codes")
         _dev(scales, torch.float16, "scales")
         _dev(zeros, torch.uint8, "zeros")
-        self.device = codes.device
-        _on(self.device, scales=scales, zeros=zeros)
+        self.device, self._index = codes.device, codes.get_device()
+        _plain(scales, torch.float16, scales.numel(), self._index, "scales")
+        _maybe(zeros, torch.uint8, scales.numel(), self._index, "zeros")
         nb = int(load().spffn_q4_packed_bytes(self.rows, self.cols, self.group,
                                               int(zeros is not None)))
         if nb == 0:
@@ -666,8 +692,8 @@ class Q4Matrix:
         self.desc = Q4Desc(packed=self.packed.data_ptr(), rows=self.rows, cols=self.cols,
                            group=self.group, zeros=int(zeros is not None))
         self._ref = C.addressof(self.desc)
-        _call(self.device, "spffn_q4_pack", codes.data_ptr(), scales.data_ptr(), _addr(zeros),
-              self.rows, self.cols, self.group, self.packed.data_ptr())
+        _call(self._index, "spffn_q4_pack", codes.data_ptr(), scales.data_ptr(),
+              None if zeros is None else zeros.data_ptr(), self.rows, self.cols, self.group, self.packed.data_ptr())
         self._need = [int(load().spffn_q4_matvec_workspace_bytes(self._ref, B))
                       for B in range(MAX_BATCH + 1)]
 
@@ -686,28 +712,25 @@ def q4_matvec(w, x, bias=None, resid=None, rms_eps=None, y=None, ws=None):
     [cols]), B <= MAX_BATCH; r is 1, or with rms_eps the gainless RMS norm's
     1 / sqrt(mean(x^2) + rms_eps) of each token.  y may be resid (in place).
     Three tokens and more take a workspace (w.workspace(B); made here if None)."""
-    B = _tokens(x, w.cols)
+    B, rows, index = _tokens(x, w.cols), w.rows, w._index
     if not 1 <= B <= MAX_BATCH:
         raise ValueError(f"{B} tokens: 1 to {MAX_BATCH}")
-    _size(bias, w.rows, "bias")
-    _size(resid, B * w.rows, "resid")
-    _size(y, B * w.rows, "y")
-    if rms_eps is not None and not rms_eps >= 0:
+    _sizes((bias, rows, "bias"), (resid, B * rows, "resid"), (y, B * rows, "y"))
+    if rms_eps is None:
+        rms_eps = -1.0
+    elif not rms_eps >= 0:
         raise ValueError(f"rms_eps={rms_eps} must be >= 0")
-    _dev(x, torch.float32, "x")
-    _dev(bias, torch.float32, "bias")
-    _dev(resid, torch.float32, "resid")
+    f32 = torch.float32
+    px = _plain(x, f32, B * w.cols, index, "x")
     if y is None:
-        y = torch.empty(x.shape[:-1] + (w.rows,), dtype=torch.float32, device=x.device)
-    _dev(y, torch.float32, "y")
-    need = w.workspace_bytes(B)
-    if need and ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=w.device)
-    nb = _ws_bytes(ws, need) if need else 0
-    _on(w.device, x=x, bias=bias, resid=resid, y=y, ws=ws)
-    _call(w.device, "spffn_q4_matvec", w._ref, x.data_ptr(), B,
-          -1.0 if rms_eps is None else float(rms_eps), _addr(bias), _addr(resid), y.data_ptr(),
-          ws.data_ptr() if need else None, nb)
+        y = torch.empty(x.shape[:-1] + (rows,), dtype=f32, device=w.device)
+    need, pw, nb = w._need[B], None, 0
+    if need:
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=w.device)
+        pw, nb = _work(ws, need, index)
+    _call(index, "spffn_q4_matvec", w._ref, px, B, rms_eps, _maybe(bias, f32, rows, index, "bias"),
+          _maybe(resid, f32, B * rows, index, "resid"), _plain(y, f32, B * rows, index, "y"), pw, nb)
     return y
 
 
@@ -723,30 +746,30 @@ def block_tables(lens, adds, table, free_list, n_free, page_size, n_tokens, star
     R = lens.numel()
     if table.dim() != 2 or table.shape[0] != R:
         raise ValueError(f"table must have shape [{R}, width], got {tuple(table.shape)}")
-    n = int(n_tokens)
+    n, i32, width = int(n_tokens), torch.int32, table.shape[1]
     if n < 0:
         raise ValueError(f"n_tokens={n_tokens} < 0")
-    _size(adds, R, "adds")
-    _size(n_free, 1, "n_free")
-    sizes = (R + 1, R, n, n, 2)
-    out = [starts, new_lens, slots, positions, left]
-    names = ("starts", "new_lens", "slots", "positions", "left")
-    for name, t, k in zip(names, out, sizes):
-        _size(t, k, name)
-    for name, t in (("lens", lens), ("adds", adds), ("table", table), ("free_list", free_list),
-                    ("n_free", n_free)):
-        _dev(t, torch.int32, name)
-    dev = lens.device
-    out = [torch.empty(k, dtype=torch.int32, device=dev) if t is None else
-           _dev(t, torch.int32, name) for name, t, k in zip(names, out, sizes)]
-    ret = dict(zip(names, out))
-    _on(dev, adds=adds, table=table, free_list=free_list, n_free=n_free, **ret)
-    # an empty free list still has an address (it is never read)
-    free = free_list.data_ptr() or n_free.data_ptr()
-    _call(dev, "spffn_block_tables", lens.data_ptr(), adds.data_ptr(), R, int(page_size),
-          table.data_ptr(), table.shape[1], free, free_list.numel(), n_free.data_ptr(),
-          *(t.data_ptr() for t in out[:4]), n, out[4].data_ptr())
-    return ret
+    _sizes((adds, R, "adds"), (n_free, 1, "n_free"), (starts, R + 1, "starts"),
+           (new_lens, R, "new_lens"), (slots, n, "slots"), (positions, n, "positions"),
+           (left, 2, "left"))
+    _dev(lens, i32, "lens")
+    dev, index, cap = lens.device, lens.get_device(), free_list.numel()
+    new = lambda k: torch.empty(k, dtype=i32, device=dev)  # noqa: E731
+    starts = new(R + 1) if starts is None else starts
+    new_lens = new(R) if new_lens is None else new_lens
+    slots = new(n) if slots is None else slots
+    positions = new(n) if positions is None else positions
+    left = new(2) if left is None else left
+    pf = _plain(n_free, i32, 1, index, "n_free")
+    _call(index, "spffn_block_tables", lens.data_ptr(), _plain(adds, i32, R, index, "adds"), R,
+          page_size, _plain(table, i32, R * width, index, "table"), width,
+          # an empty free list still has an address (it is never read)
+          _plain(free_list, i32, cap, index, "free_list") or pf, cap, pf,
+          _plain(starts, i32, R + 1, index, "starts"), _plain(new_lens, i32, R, index, "new_lens"),
+          _plain(slots, i32, n, index, "slots"), _plain(positions, i32, n, index, "positions"), n,
+          _plain(left, i32, 2, index, "left"))
+    return {"starts": starts, "new_lens": new_lens, "slots": slots, "positions": positions,
+            "left": left}
 
 
 class KVCache:
@@ -776,14 +799,13 @@ class KVCache:
         _size(k_scale, self.kv_heads, "k_scale")
         _size(v_scale, self.kv_heads, "v_scale")
         _dev(k, None, "k")
-        _dev(v, k.dtype, "v")
-        _dev(k_scale, torch.float32, "k_scale")
-        _dev(v_scale, torch.float32, "v_scale")
-        self.device = k.device
-        _on(self.device, v=v, k_scale=k_scale, v_scale=v_scale)
+        self.device, self._index = k.device, k.get_device()
+        _plain(v, k.dtype, v.numel(), self._index, "v")
+        ps, pv = (_maybe(t, torch.float32, self.kv_heads, self._index, name)
+                  for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")))
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.desc = CacheDesc(k=k.data_ptr(), v=v.data_ptr(), k_scale=_addr(k_scale),
-                              v_scale=_addr(v_scale), pages=self.pages, page_size=self.page_size,
+        self.desc = CacheDesc(k=k.data_ptr(), v=v.data_ptr(), k_scale=ps, v_scale=pv,
+                              pages=self.pages, page_size=self.page_size,
                               kv_heads=self.kv_heads, head_dim=self.head_dim,
                               dtype=_CACHE_DTYPES[k.dtype])
         self._ref = C.addressof(self.desc)
@@ -807,36 +829,39 @@ class KVCache:
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 
 
-def _token_rows(t, name, heads, dim):
+def _token_rows(t, name, heads, dim, index):
     """Check [N, heads, dim] rows whose tokens may be strided; the stride in elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must have shape [N, {heads}, {dim}], got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must have shape [N, {heads}, {dim}], got {tuple(shape)}")
+    if t.get_device() != index:
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
     if t.dtype not in _ROW_DTYPES:
         raise TypeError(f"{name} must be float32 or float16, got {t.dtype}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    by_token, by_head, by_dim = t.stride()
+    if by_dim != 1 or (heads > 1 and by_head != dim):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    return by_token if shape[0] > 1 else heads * dim
 
 
 def kv_append(cache, k, v, slots):
     """Writes rows k, v [N, kv_heads, head_dim] (fp32 or fp16; the tokens may be
     strided, as parts of a fused projection are) to the cache slots int32 [N];
     tokens of slot -1 are skipped."""
-    ld_k = _token_rows(k, "k", cache.kv_heads, cache.head_dim)
-    ld_v = _token_rows(v, "v", cache.kv_heads, cache.head_dim)
+    index, heads, dim = cache._index, cache.kv_heads, cache.head_dim
+    ld_k = _token_rows(k, "k", heads, dim, index)
+    ld_v = _token_rows(v, "v", heads, dim, index)
     N = k.shape[0]
-    if v.shape[0] != N or v.dtype != k.dtype:
+    if v.shape[0] != N or v.dtype is not k.dtype:
         raise ValueError("k and v must hold as many tokens of one dtype")
-    _size(slots, N, "slots")
-    _dev(slots, torch.int32, "slots")
-    _on(cache.device, k=k, v=v, slots=slots)
+    ps = _plain(slots, torch.int32, N, index, "slots")
     if N:
-        _call(cache.device, "spffn_kv_append", cache._ref, k.data_ptr(), v.data_ptr(),
-              _ROW_DTYPES[k.dtype], ld_k, ld_v, slots.data_ptr(), N)
+        _call(index, "spffn_kv_append", cache._ref, k.data_ptr(), v.data_ptr(),
+              _ROW_DTYPES[k.dtype], ld_k, ld_v, ps, N)
 
 
 def tree_attention(cache, q, starts, lens, table, mask=None, scale=None, max_new=None, out=None,
@@ -851,36 +876,32 @@ def tree_attention(cache, q, starts, lens, table, mask=None, scale=None, max_new
     are left as they were."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must have shape [N, heads, head_dim]")
-    N, heads = q.shape[0], q.shape[1]
+    index, dim, dtype = cache._index, cache.head_dim, q.dtype
+    N, heads, _ = q.shape
     if heads < 1 or heads % cache.kv_heads:
         raise ValueError(f"heads={heads} is no multiple of kv_heads={cache.kv_heads}")
     R = lens.numel()
-    _size(starts, R + 1, "starts")
-    _size(mask, N, "mask")
+    _sizes((starts, R + 1, "starts"), (mask, N, "mask"))
     if table.dim() != 2 or table.shape[0] != R:
         raise ValueError(f"table must have shape [{R}, width], got {tuple(table.shape)}")
+    width, i32 = table.shape[1], torch.int32
     max_new = min(max(N, 1), MAX_NEW) if max_new is None else int(max_new)
-    ld_q = _token_rows(q, "q", heads, cache.head_dim)
+    ld_q = _token_rows(q, "q", heads, dim, index)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ld_out = _token_rows(out, "out", heads, cache.head_dim)
-    if out.shape[0] != N or out.dtype != q.dtype:
+        out = torch.empty(q.shape, dtype=dtype, device=cache.device)
+    ld_out = _token_rows(out, "out", heads, dim, index)
+    if out.shape[0] != N or out.dtype is not dtype:
         raise ValueError("out must hold as many tokens as q, of its dtype")
-    _dev(starts, torch.int32, "starts")
-    _dev(lens, torch.int32, "lens")
-    _dev(table, torch.int32, "table")
-    _dev(mask, torch.int64, "mask")
-    dev = cache.device
-    _on(dev, q=q, out=out, starts=starts, lens=lens, table=table, mask=mask)
+    p_starts, p_lens = _plain(starts, i32, R + 1, index, "starts"), _plain(lens, i32, R, index, "lens")
+    p_table = _plain(table, i32, R * width, index, "table")
+    p_mask = _maybe(mask, torch.int64, N, index, "mask")
     if ws is None:
-        ws = cache.workspace(heads, max_new, q.dtype)
-    nb = _ws_bytes(ws, cache.workspace_bytes(heads, max_new, q.dtype))
-    _on(dev, ws=ws)
+        ws = cache.workspace(heads, max_new, dtype)
+    pw, nb = _work(ws, cache.workspace_bytes(heads, max_new, dtype), index)
     if N:
-        _call(dev, "spffn_tree_attention", cache._ref, q.data_ptr(), _ROW_DTYPES[q.dtype], ld_q, N,
-              heads, starts.data_ptr(), lens.data_ptr(), table.data_ptr(), R, table.shape[1],
-              _addr(mask), max_new, cache.head_dim ** -0.5 if scale is None else float(scale),
-              out.data_ptr(), ld_out, ws.data_ptr(), nb)
+        _call(index, "spffn_tree_attention", cache._ref, q.data_ptr(), _ROW_DTYPES[dtype], ld_q, N,
+              heads, p_starts, p_lens, p_table, R, width, p_mask, max_new,
+              dim ** -0.5 if scale is None else scale, out.data_ptr(), ld_out, pw, nb)
     return out
 
 

@@ -219,8 +219,7 @@ def test_q4_matrix_needs_a_device():
 
 
 class FakeMatrix:
-    rows, cols, device = 8, 64, torch.device("cuda:0")
-    workspace_bytes = staticmethod(lambda B: 0)
+    rows, cols, device, _index, _need = 8, 64, torch.device("cuda:0"), 0, [0] * 17
 
 
 @pytest.mark.parametrize("x,kw", [
@@ -270,7 +269,7 @@ def test_kv_cache_dtype():
 
 
 class FakeCache:
-    kv_heads, head_dim, device = 2, 64, torch.device("cuda:0")
+    kv_heads, head_dim, device, _index = 2, 64, torch.device("cuda:0"), 0
 
 
 def test_rows_and_counts():
