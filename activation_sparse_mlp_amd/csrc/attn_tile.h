@@ -365,6 +365,19 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
         const int col0 = (qt * WQ + wq) * C::COLS;
         const int32_t *trow = a.table + (size_t)r * a.width;
 
+        // A step covers TT blocks of 16 tokens, each on one page: lane b (mod TT) holds block b's.
+        // No load here hangs on a condition: one that may be skipped would make the loads
+        // behind it be waited for as if it had been.  What is not wanted is read twice.
+        auto pages_of = [&](int st) {
+            const int tok = st * TS + 16 * (lane & (TT - 1));
+            const int pg = trow[(tok < rq.tot ? tok : rq.tot - 1) >> a.shift];
+            return tok < rq.tot ? pg : -1;
+        };
+        auto next = [&](int st) { return st + WK < s1 ? st + WK : st; };
+        int st = s0 + wk;
+        const int first = st < s1 ? st : s1 - 1;  // (a wave without a step reads and drops one)
+        int pg0 = pages_of(first), pg1 = pages_of(next(first));  // pages of this step and the next
+
         // ---- queries as B operands ----
         half8 qr[C::QLDS ? 1 : C::PL][C::QLDS ? 1 : NQ][C::QLDS ? 1 : C::KS];
         half8 *qs = reinterpret_cast<half8 *>(lds) + (size_t)wv * (C::QBYTES / 64) + lane;
@@ -474,15 +487,6 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
         const uint64_t kstride = (uint64_t)a.H * ((size_t)C::NPK << a.shift) * 16;  // bytes per page
         const uint64_t vstride = (uint64_t)a.H * (ps / E) * D * 16;
         u32x4_t kp[TT][KP], vp[DT];
-        // A step covers TT blocks of 16 tokens, each on one page: lane b (mod TT) holds block b's.
-        // No load here hangs on a condition: one that may be skipped would make the loads
-        // behind it be waited for as if it had been.  What is not wanted is read twice.
-        auto pages_of = [&](int st) {
-            const int tok = st * TS + 16 * (lane & (TT - 1));
-            const int pg = trow[(tok < rq.tot ? tok : rq.tot - 1) >> a.shift];
-            return tok < rq.tot ? pg : -1;
-        };
-        auto next = [&](int st) { return st + WK < s1 ? st + WK : st; };
         auto there = [&](int pg) { return (uint32_t)pg < (uint32_t)a.pages; };
         auto load_k = [&](int st, int pgs) {  // a page that is not there reads page 0 (and is masked)
 #pragma unroll
@@ -512,9 +516,6 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
 #pragma unroll
             for (int d = 0; d < DT; ++d) vp[d] = fetch<C::ONCE>(vb + d * 256);
         };
-        int st = s0 + wk;
-        const int first = st < s1 ? st : s1 - 1;  // (a wave without a step reads and drops one)
-        int pg0 = pages_of(first), pg1 = pages_of(next(first));  // pages of this step and the next
         __builtin_amdgcn_sched_barrier(0);  // in this order, or the loop waits for both at once
         load_k(first, pg0);
         __builtin_amdgcn_sched_barrier(0);
@@ -834,25 +835,51 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
     if (threadIdx.x == 0) a.tasks[blockIdx.x] = task;
 }
 
-// Joins the slots of the unit that workgroup blockIdx.x of the attention
-// launch began and did not finish (its task): slot 2w + 1 holds the first part,
-// the following workgroups' slots 2w' the rest.  A thread takes four outputs of
-// a column and every JP-th part, four parts at a time so that their loads are in
-// flight together; the JP sums of a column are then added in order.
+// Joins the parts of the units that the attention launch dealt to several
+// workgroups (its tasks): for a task of workgroup w, slot 2w + 1 holds the first
+// part, the following workgroups' slots 2w' the rest.  Every workgroup gathers
+// the tasks there are (at most one per workgroup of the first launch, usually
+// one per unit) and takes its share of all their columns, JC at a time: a
+// thread four outputs of a column and every JP-th part, four parts at a time so
+// that their loads are in flight together; the JP sums of a column are then
+// added in order.
 constexpr int kJoinParts = 4;
-constexpr int kJoinRows = 16;  // workgroups that share a unit's columns, at most
+constexpr int kJoinWgs = 1024;
 
 template <bool FP8, bool Q16, int D>
-__global__ __launch_bounds__(kThreads) void attend_join_kernel(Args a, int cw) {
+__global__ __launch_bounds__(kThreads) void attend_join_kernel(Args a, int wgs, int cw) {
     constexpr int JP = kJoinParts, TC = D / 4;  // threads per column and part group
     constexpr int JC = kThreads / (TC * JP);    // columns at a time
     __shared__ Sum part[JP][JC][TC];
-    const int w = blockIdx.x;
-    const Task task = a.tasks[w];
-    if (task.more == 0) return;
+    __shared__ uint16_t list[kMaxWgs];
+    __shared__ int count[kMaxWgs / 64];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    // ---- the tasks, in order ----
+    uint64_t have[kMaxWgs / kThreads];
+#pragma unroll
+    for (int k = 0; k < kMaxWgs / kThreads; ++k) {
+        const int w = k * kThreads + threadIdx.x;
+        have[k] = __ballot(w < wgs && a.tasks[w < wgs ? w : 0].more > 0);
+        if (lane == 0) count[k * (kThreads / 64) + wv] = __popcll(have[k]);
+    }
+    __syncthreads();
+    int n_tasks = 0;
+#pragma unroll
+    for (int k = 0; k < kMaxWgs / kThreads; ++k) {
+        int before = 0;
+        for (int x = 0; x < k * (kThreads / 64) + wv; ++x) before += count[x];
+        if ((have[k] >> lane) & 1)
+            list[before + __popcll(have[k] & ((1ull << lane) - 1))] = (uint16_t)(k * kThreads + threadIdx.x);
+    }
+    for (int x = 0; x < kMaxWgs / 64; ++x) n_tasks += count[x];
+    __syncthreads();
+    // ---- a share of their columns ----
+    const int rows = (cw + JC - 1) / JC;
     const int d4 = threadIdx.x % TC, jc = (threadIdx.x / TC) % JC, jp = threadIdx.x / (TC * JC);
-    for (int c0 = blockIdx.y * JC; c0 < cw; c0 += gridDim.y * JC) {
-        const int c = c0 + jc, cg = task.qt * cw + c;
+    for (int item = blockIdx.x; item < n_tasks * rows; item += gridDim.x) {
+        const int w = list[item / rows], c = item % rows * JC + jc;
+        const Task task = a.tasks[w];
+        const int cg = task.qt * cw + c;
         const bool real = c < cw && cg < task.n_cols && jp < JP;  // (96 dimensions leave threads over)
         Sum acc{kNegInf, 0.0f, f32x4{0.f, 0.f, 0.f, 0.f}};
         if (real) {
@@ -899,10 +926,7 @@ hipError_t launch_mode(const Args &a, hipStream_t s) {
     fn<<<C::WGS, kThreads, lds, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    constexpr int jc = kThreads / (D / 4 * kJoinParts);
-    const int cw = C::COLS * a.wq, rows = (cw + jc - 1) / jc;
-    attend_join_kernel<FP8, Q16, D>
-        <<<dim3(C::WGS, rows < kJoinRows ? rows : kJoinRows), kThreads, 0, s>>>(a, cw);
+    attend_join_kernel<FP8, Q16, D><<<kJoinWgs, kThreads, 0, s>>>(a, C::WGS, C::COLS * a.wq);
     return hipGetLastError();
 }
 
