@@ -61,13 +61,17 @@ constexpr int kThreads = 256;
 // requests of 96 heads: 397 us with 0, 313 with 4, 287 with 8 and with 16.
 constexpr int kSetup = 8;
 
+// A share is at least this many steps: with less, starting more workgroups and
+// joining more parts costs more than it saves (one request of 4096 tokens and 8
+// kv heads: 18.1 us with 4, 15.4 with 8, 19.0 with 16).
+constexpr int kMinShare = 8;
+
 enum Mode : int { kHalf = 0, kOne = 1, kTwo = 2 };  // columns per wave: 8, 16, 32
 
-// What the second launch has to join for a workgroup of the first: the parts
-// of this many workgroups after it (0: nothing), of request tokens from a0 on.
+// What the second launch has to join for a workgroup of the first: its unit,
+// and (an array of its own) of how many workgroups after it the unit has parts.
 struct Task {
-    int more, a0, n_cols, h, qt;
-    int pad[3];
+    int a0, n_cols, h, qt;
 };
 
 struct Args {
@@ -79,9 +83,11 @@ struct Args {
     const int64_t *mask;
     float *part_o, *part_ml;
     Task *tasks;
+    int *more;
     int64_t ldq, ldo;
     float scale;
     int N, R, G, H, width, pages, shift, max_new;
+    int narrow;  // R <= 64 and every position fits 31 bits
     int wq;  // waves along the columns (1, 2, 4); 4 / wq along the tokens
 };
 
@@ -141,9 +147,26 @@ __device__ __forceinline__ Req uniform(const Req &q) {
                uniform(q.span), uniform(q.nqt)};
 }
 
+// Inclusive sum over the lanes, by lane shifts within rows of 16 and two
+// broadcasts across them.
+__device__ __forceinline__ int scan32(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31
+    return v;
+}
+
 // Every wave computes the plan for itself: the total and each workgroup's share.
 template <int TS>
 __device__ __forceinline__ int64_t plan_total(const Args &a, int cw, int lane, int64_t &incl0) {
+    if (a.narrow) {  // up to 64 requests, their sum in 32 bits
+        const int incl = scan32((int)req_steps<TS>(a, lane, cw));
+        incl0 = incl;
+        return __builtin_amdgcn_readlane(incl, 63);
+    }
     int64_t total = 0;
     for (int b = 0; b < a.R; b += 64) {
         const int64_t incl = scan64(req_steps<TS>(a, b + lane, cw), lane);
@@ -157,6 +180,12 @@ __device__ __forceinline__ int64_t plan_total(const Args &a, int cw, int lane, i
 template <int TS>
 __device__ __forceinline__ int plan_find(const Args &a, int cw, int lane, int64_t incl0, int64_t p,
                                          int64_t &base) {
+    if (a.narrow) {
+        const int incl = (int)incl0;
+        const int i = __ffsll((long long)__ballot((int)p < incl)) - 1;
+        base = i ? __builtin_amdgcn_readlane(incl, i - 1) : 0;
+        return i;
+    }
     int64_t before = 0;
     for (int b = 0; b < a.R; b += 64) {
         const int64_t incl =
@@ -179,6 +208,7 @@ constexpr int kMaxWgs = 768;  // of a launch
 template <int WGS>
 __device__ __forceinline__ int64_t share(int64_t total, int wk) {
     const int64_t c = (int64_t)((uint64_t)(total + WGS - 1) / (uint64_t)WGS);
+    if (c < kMinShare) return kMinShare;
     return (c + wk - 1) & ~(int64_t)(wk - 1);
 }
 
@@ -343,9 +373,9 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
     const int64_t per = share<C::WGS>(total, WK);
     int64_t p = (int64_t)blockIdx.x * per;
     const int64_t end = p + per < total ? p + per : total;
-    Task task{};
+    int more = 0;
     if (p >= end) {
-        if (threadIdx.x == 0) a.tasks[blockIdx.x] = task;
+        if (threadIdx.x == 0) a.more[blockIdx.x] = 0;
         return;
     }
     int r = plan_find<TS>(a, cw, lane, incl0, p, base);
@@ -816,8 +846,10 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
             }
         }
         // a unit begun here and not finished: the workgroups after this one that go on with it
-        if (s0 == 0 && !whole)
-            task = Task{(int)((rq.span - x1 + per - 1) / per), rq.a0, n_cols, h, qt, {}};
+        if (s0 == 0 && !whole) {
+            more = per >= rq.span - x1 ? 1 : (rq.span - x1 + (int)per - 1) / (int)per;
+            if (threadIdx.x == 0) a.tasks[blockIdx.x] = Task{rq.a0, n_cols, h, qt};
+        }
 
         // ---- next segment ----
         p += x1 - x0;
@@ -832,7 +864,7 @@ __global__ __launch_bounds__(kThreads, (Cfg<FP8, Q16, D, MODE>::WAVES)) void att
             } while (rsteps == 0);
         }
     }
-    if (threadIdx.x == 0) a.tasks[blockIdx.x] = task;
+    if (threadIdx.x == 0) a.more[blockIdx.x] = more;
 }
 
 // Joins the parts of the units that the attention launch dealt to several
@@ -859,7 +891,7 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(Args a, int wgs, 
 #pragma unroll
     for (int k = 0; k < kMaxWgs / kThreads; ++k) {
         const int w = k * kThreads + threadIdx.x;
-        have[k] = __ballot(w < wgs && a.tasks[w < wgs ? w : 0].more > 0);
+        have[k] = __ballot(w < wgs && a.more[w < wgs ? w : 0] > 0);
         if (lane == 0) count[k * (kThreads / 64) + wv] = __popcll(have[k]);
     }
     __syncthreads();
@@ -879,16 +911,17 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(Args a, int wgs, 
     for (int item = blockIdx.x; item < n_tasks * rows; item += gridDim.x) {
         const int w = list[item / rows], c = item % rows * JC + jc;
         const Task task = a.tasks[w];
+        const int more = a.more[w];
         const int cg = task.qt * cw + c;
         const bool real = c < cw && cg < task.n_cols && jp < JP;  // (96 dimensions leave threads over)
         Sum acc{kNegInf, 0.0f, f32x4{0.f, 0.f, 0.f, 0.f}};
         if (real) {
-            for (int i = jp; i <= task.more; i += 4 * JP) {
+            for (int i = jp; i <= more; i += 4 * JP) {
                 float m[4], l[4];
                 f32x4 o[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int x = i + k * JP <= task.more ? i + k * JP : i;
+                    const int x = i + k * JP <= more ? i + k * JP : i;
                     const size_t at = (size_t)(2 * (w + x) + (x == 0 ? 1 : 0)) * cw + c;
                     m[k] = a.part_ml[at * 2];
                     l[k] = a.part_ml[at * 2 + 1];
@@ -896,13 +929,13 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(Args a, int wgs, 
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (i + k * JP <= task.more) join(acc, m[k], l[k], o[k]);
+                    if (i + k * JP <= more) join(acc, m[k], l[k], o[k]);
             }
             part[jp][jc][d4] = acc;
         }
         __syncthreads();
         if (real && jp == 0) {
-            const int parts = task.more + 1 < JP ? task.more + 1 : JP;
+            const int parts = more + 1 < JP ? more + 1 : JP;
             for (int k = 1; k < parts; ++k)
                 join(acc, part[k][jc][d4].m, part[k][jc][d4].l, part[k][jc][d4].o);
             store_out<Q16, D>(a, task.a0, task.h, cg, d4 * 4, acc.o, acc.m, acc.l,

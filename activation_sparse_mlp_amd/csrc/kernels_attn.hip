@@ -30,7 +30,7 @@ Shape attn_shape(int G, int dim, int max_new, bool q16) {
 
 size_t attn_ws_bytes(int heads, int kv_heads, int dim, int max_new, bool q16) {
     const Shape sh = attn_shape(heads / kv_heads, dim, max_new, q16);
-    return (size_t)2 * attn::kMaxWgs * sh.cols * (dim + 2) * 4 + attn::kMaxWgs * sizeof(attn::Task);
+    return (size_t)2 * attn::kMaxWgs * sh.cols * (dim + 2) * 4 + attn::kMaxWgs * (sizeof(attn::Task) + sizeof(int));
 }
 
 hipError_t launch_tree_attention(const KvCache &c, const AttnCall &q, void *ws, hipStream_t s) {
@@ -50,6 +50,7 @@ hipError_t launch_tree_attention(const KvCache &c, const AttnCall &q, void *ws, 
     a.part_o = static_cast<float *>(ws);
     a.part_ml = a.part_o + (size_t)2 * attn::kMaxWgs * sh.cols * c.D;
     a.tasks = reinterpret_cast<attn::Task *>(a.part_ml + (size_t)4 * attn::kMaxWgs * sh.cols);
+    a.more = reinterpret_cast<int *>(a.tasks + attn::kMaxWgs);
     a.ldq = q.ldq;
     a.ldo = q.ldo;
     a.scale = q.scale;
@@ -61,6 +62,10 @@ hipError_t launch_tree_attention(const KvCache &c, const AttnCall &q, void *ws, 
     a.pages = c.pages;
     a.shift = c.shift;
     a.max_new = q.max_new;
+    // at most this many positions: every table row full, every request max_new tokens
+    const int64_t steps = (((int64_t)q.width << c.shift) + 31) / 32 + attn::kSetup;
+    const int64_t groups = ((int64_t)q.max_new * G + sh.cols - 1) / sh.cols;
+    a.narrow = q.R <= 64 && steps * groups * c.H * q.R < (int64_t)1 << 31;
     a.wq = sh.wq;
     return c.fp8 ? launch_attend_fp8(a, q.q16, c.D, sh.mode, s)
                  : launch_attend_f16(a, q.q16, c.D, sh.mode, s);

@@ -292,17 +292,21 @@ __global__ __launch_bounds__(64 * W) void q4mv_kernel(Q4Args a) {
     for (int d = 0; d < DW; ++d)
         if (wv + d * W < a.kb_n) load_w(d, wv + d * W);
 
-    for (int kb0 = wv; kb0 < a.kb_n; kb0 += U * W) {
+    // U blocks from kb0 on.  ALL: they and the DW after them are all there, so no load hangs
+    // on a condition (one that may be skipped would make the ones behind it be waited for as
+    // if it had been).
+    auto blocks = [&](auto all, int kb0) {
+        constexpr bool ALL = decltype(all)::value;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int kb = kb0 + u * W;
-            if (kb >= a.kb_n) break;
+            if (!ALL && kb >= a.kb_n) break;
             if (u % XB == 0) {
                 // ---- split the next XB blocks of activations ----
                 uint32_t m[XB], top = 0;
 #pragma unroll
                 for (int b = 0; b < XB; ++b) {
-                    if (b > 0 && kb + b * W >= a.kb_n) {
+                    if (!ALL && b > 0 && kb + b * W >= a.kb_n) {
 #pragma unroll
                         for (int e = 0; e < E; ++e) cx[b][e] = 0.0f;
                     }
@@ -354,8 +358,11 @@ __global__ __launch_bounds__(64 * W) void q4mv_kernel(Q4Args a) {
                     if (el == 0) reinterpret_cast<float *>(xl + B * kXPitch)[tok] = scale_down(eb);
                 }
 #pragma unroll
-                for (int b = 0; b < XB; ++b)
-                    if (kb + (XB + b) * W < a.kb_n) load_x(b, kb + (XB + b) * W);
+                for (int b = 0; b < XB; ++b) {
+                    const int kx = kb + (XB + b) * W;
+                    if (ALL) load_x(b, kx < a.kb_n ? kx : kb);
+                    else if (kx < a.kb_n) load_x(b, kx);
+                }
                 __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
                 __builtin_amdgcn_wave_barrier();
                 __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -383,9 +390,12 @@ __global__ __launch_bounds__(64 * W) void q4mv_kernel(Q4Args a) {
                         acc[t][j] = fmaf(z[j], fmaf((float)cs[u % DW][t][i][j], f, 0.0f), acc[t][j]);
                 }
             }
-            if (kb + DW * W < a.kb_n) load_w(u % DW, kb + DW * W);
+            if (ALL || kb + DW * W < a.kb_n) load_w(u % DW, kb + DW * W);
         }
-    }
+    };
+    int kb0 = wv;
+    for (; kb0 + (U + DW - 1) * W < a.kb_n; kb0 += U * W) blocks(std::true_type{}, kb0);
+    for (; kb0 < a.kb_n; kb0 += U * W) blocks(std::false_type{}, kb0);
 
     // ---- fixed-order sum over the workgroup's waves, scale, bias, residual ----
     __syncthreads();
@@ -580,11 +590,12 @@ __global__ __launch_bounds__(64 * W) void q4mm_kernel(MmArgs ma) {
 #pragma unroll
     for (int d = 0; d < DW; ++d)
         if (wv + d * W < a.kb_n) load_w(d, wv + d * W);
-    for (int kb0 = wv; kb0 < a.kb_n; kb0 += DW * W) {
+    auto blocks = [&](auto all, int kb0) {  // as in q4mv_kernel
+        constexpr bool ALL = decltype(all)::value;
 #pragma unroll
         for (int u = 0; u < DW; ++u) {
             const int kb = kb0 + u * W;
-            if (kb >= a.kb_n) break;
+            if (!ALL && kb >= a.kb_n) break;
             const int kx = kb + W < a.kb_n ? kb + W : kb;  // the last block's are loaded again
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
@@ -610,9 +621,12 @@ __global__ __launch_bounds__(64 * W) void q4mm_kernel(MmArgs ma) {
                     for (int j = 0; j < 4; ++j)
                         acc[t][j] = fmaf(z[t][j], (float)cs[u][t][i][j], acc[t][j]);
             }
-            if (kb + DW * W < a.kb_n) load_w(u, kb + DW * W);
+            if (ALL || kb + DW * W < a.kb_n) load_w(u, kb + DW * W);
         }
-    }
+    };
+    int kb0 = wv;
+    for (; kb0 + (2 * DW - 1) * W < a.kb_n; kb0 += DW * W) blocks(std::true_type{}, kb0);
+    for (; kb0 < a.kb_n; kb0 += DW * W) blocks(std::false_type{}, kb0);
 #pragma unroll
     for (int t = 0; t < RT; ++t)
         *reinterpret_cast<f32x4 *>(red + ((wv * RT + t) * 16 + n) * 16 + 4 * g) = acc[t];
