@@ -906,7 +906,7 @@ spffn_status spffn_q4_pack(const uint8_t *codes, const void *scales, const uint8
 
 size_t spffn_q4_matvec_workspace_bytes(const spffn_q4_matrix *w, int32_t B) {
     if (!w || !q4_sizes_ok(w->rows, w->cols, w->group) || B < 1 || B > SPFFN_MAX_BATCH) return 0;
-    return q4_ws_bytes(w->cols, B);
+    return q4_ws_bytes(w->rows, w->cols, B);
 }
 
 spffn_status spffn_q4_matvec(const spffn_q4_matrix *w, const float *x, int32_t B, float rms_eps,
@@ -929,7 +929,7 @@ spffn_status spffn_q4_matvec(const spffn_q4_matrix *w, const float *x, int32_t B
     if ((resid && resid != y && overlap(y, ny, resid, ny)) ||
         (bias && overlap(y, ny, bias, (size_t)w->rows * 4)))
         return fail(SPFFN_E_ARG, "q4_matvec: y overlaps bias or part of resid");
-    if (const size_t need = q4_ws_bytes(w->cols, B))
+    if (const size_t need = q4_ws_bytes(w->rows, w->cols, B))
         if (spffn_status st = check_ws(need, ws, ws_bytes)) return st;
     SPFFN_HIP(launch_q4_matvec(static_cast<const uint8_t *>(w->packed), w->rows, w->cols, w->group,
                                w->zeros != 0, x, B, rms_eps, bias, resid, y, ws,

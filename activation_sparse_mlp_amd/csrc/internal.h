@@ -180,7 +180,7 @@ hipError_t launch_q4_pack(const uint8_t *codes, const uint16_t *scales, const ui
 hipError_t launch_q4_matvec(const uint8_t *packed, int rows, int cols, int group, bool zeros,
                             const float *x, int B, float eps, const float *bias,
                             const float *resid, float *y, void *ws, hipStream_t s);
-size_t q4_ws_bytes(int cols, int B);  // 0: none needed
+size_t q4_ws_bytes(int rows, int cols, int B);  // 0: none needed
 
 // Paged key/value cache (kernels_paged.hip); page_size = 1 << shift.
 struct KvCache {

@@ -32,8 +32,8 @@
 // Packed layout (launch_q4_pack): per tile of 16 rows and block of 128 columns
 // 1 KiB of codes in the order of one wave's 16-byte loads -- lane l = 16 g + m
 // holds row m, word w the eight columns 32 w + 8 g + e, code 2i in nibble i and
-// code 2i + 1 in nibble i + 4 -- then all scales [tile, block, group, 16] fp16,
-// then all zero points (same shape, bytes).  Rows and columns are padded with
+// code 2i + 1 in nibble i + 4 -- then all scales [tile, block, row, group] fp16,
+// then all zero points (same shape, bytes): a lane's are one load each.  Rows and columns are padded with
 // zero codes and zero scales.
 #include "device.h"
 
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t *__restrict_
         const int gi = lane >> 4, gg = kb * ng + gi;
         const bool in = row < rows && gg < groups;
         uint16_t *sc = reinterpret_cast<uint16_t *>(packed + (size_t)n_rec * 1024);
-        const size_t at = ((size_t)rec * ng + gi) * 16 + m;
+        const size_t at = ((size_t)rec * 16 + m) * ng + gi;
         sc[at] = in ? scales[(size_t)row * groups + gg] : (uint16_t)0;
         if (zeros)
             packed[(size_t)n_rec * (1024 + 32 * ng) + at] =
@@ -129,11 +129,48 @@ struct Offsets {
     half2v one, sixteen;
     template <bool ZP>
     __device__ __forceinline__ static Offsets of(uint32_t z) {
-        const _Float16 zp = ZP ? (_Float16)(float)z : (_Float16)8.0f;
+        const _Float16 zp = ZP ? (_Float16)(float)(z & 15u) : (_Float16)8.0f;
         const _Float16 a = (_Float16)-1024.0f - zp, b = (_Float16)-64.0f - zp;
         return Offsets{half2v{a, a}, half2v{b, b}};
     }
 };
+
+// A lane needs the scales of rows 4g .. 4g + 3 of a record, as every lane of its
+// row of 16 does.  It loads those of one, 4g + n % 4, and takes the others from
+// the lanes of its quad: a quarter of the bytes through the load path, where
+// whole loads of the same four rows by every lane cost as much as the codes.
+template <int NG>
+struct Scales {
+    static constexpr int DW = NG < 2 ? 1 : NG / 2;
+    uint32_t own[DW];
+    __device__ __forceinline__ void load(const uint8_t *p) {
+        if constexpr (NG == 1) own[0] = *reinterpret_cast<const uint16_t *>(p);
+        else if constexpr (NG == 2) own[0] = *reinterpret_cast<const uint32_t *>(p);
+        else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(p);
+            own[0] = x.x;
+            own[1] = x.y;
+        }
+    }
+    template <int ROW>
+    __device__ __forceinline__ half2v quad(int dw) const {  // row 4g + ROW, groups 2 dw, 2 dw + 1
+        return __builtin_bit_cast(half2v, __builtin_amdgcn_mov_dpp((int)own[dw], ROW * 0x55, 0xF, 0xF, true));
+    }
+    __device__ __forceinline__ _Float16 operator()(int row, int group) const {
+        const int dw = group / 2;
+        const half2v x = row == 0 ? quad<0>(dw) : row == 1 ? quad<1>(dw) : row == 2 ? quad<2>(dw)
+                                                                                    : quad<3>(dw);
+        return x[group % 2];
+    }
+};
+
+// The NG zero points of a row, a byte each.
+template <int NG>
+__device__ __forceinline__ uint32_t load_zeros(const uint8_t *p) {
+    if constexpr (NG == 1) return *p;
+    else if constexpr (NG == 2) return *reinterpret_cast<const uint16_t *>(p);
+    else return *reinterpret_cast<const uint32_t *>(p);
+}
 
 // Eight codes as q - z.
 __device__ __forceinline__ half8 widen(uint32_t w, const CodeBits &bits, const Offsets &off) {
@@ -213,7 +250,7 @@ __device__ __forceinline__ float sum_waves(const float *red, int b, int t, int r
 // blocks at a time (a scale per token and block), through LDS of its own.
 // ---------------------------------------------------------------------------
 template <int NG, bool ZP, int B, int RT, int W, int DW>
-__global__ __launch_bounds__(64 * W) void q4mv_kernel(Q4Args a) {
+__global__ __launch_bounds__(64 * W, 4) void q4mv_kernel(Q4Args a) {
     constexpr int E = 2 * B;                  // activations per lane and block
     constexpr int XB = 4 / B;
     constexpr int LPT = kBlk / E;             // lanes per token
@@ -250,8 +287,8 @@ __global__ __launch_bounds__(64 * W) void q4mv_kernel(Q4Args a) {
     for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     uint4 cw[DW][RT];
-    half4 cs[DW][RT][NG];
-    uint32_t cz[DW][RT][NG];
+    Scales<NG> cs[DW][RT];
+    uint32_t cz[DW][RT];
     float cx[XB][E];
     auto load_w = [&](int st, int kb) {
 #pragma unroll
@@ -260,12 +297,8 @@ __global__ __launch_bounds__(64 * W) void q4mv_kernel(Q4Args a) {
             cw[st][t] = __builtin_bit_cast(
                 uint4, __builtin_nontemporal_load(
                            reinterpret_cast<const u32x4_t *>(a.packed + rec * 1024) + lane));
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                cs[st][t][i] =
-                    *reinterpret_cast<const half4 *>(sc_base + (rec * NG + i) * 32 + g * 8);
-                if (ZP) cz[st][t][i] = zp_base[(rec * NG + i) * 16 + n];
-            }
+            cs[st][t].load(sc_base + (rec * 16 + 4 * g + (n & 3)) * (2 * NG));
+            if (ZP) cz[st][t] = load_zeros<NG>(zp_base + (rec * 16 + n) * NG);
         }
     };
     auto load_x = [&](int xb, int kb) {
@@ -379,7 +412,7 @@ __global__ __launch_bounds__(64 * W) void q4mv_kernel(Q4Args a) {
                 const uint32_t words[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                 for (int i = 0; i < NG; ++i) {
-                    const Offsets off = Offsets::of<ZP>(cz[u % DW][t][i]);
+                    const Offsets off = Offsets::of<ZP>(cz[u % DW][t] >> (8 * i));
                     f32x4 z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int w = i * SPG; w < (i + 1) * SPG; ++w)
@@ -387,7 +420,7 @@ __global__ __launch_bounds__(64 * W) void q4mv_kernel(Q4Args a) {
                                                                    0, 0, 0);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        acc[t][j] = fmaf(z[j], fmaf((float)cs[u % DW][t][i][j], f, 0.0f), acc[t][j]);
+                        acc[t][j] = fmaf(z[j], fmaf((float)cs[u % DW][t](j, i), f, 0.0f), acc[t][j]);
                 }
             }
             if (ALL || kb + DW * W < a.kb_n) load_w(u % DW, kb + DW * W);
@@ -444,6 +477,8 @@ struct SplitArgs {
     float *fac;
     int cols, kb_n, wide;
     float eps;
+    int *done;
+    int n_done;  // counters of the product's launch, to be cleared
 };
 
 __global__ __launch_bounds__(kSplitThreads) void q4_split_kernel(SplitArgs a) {
@@ -451,6 +486,7 @@ __global__ __launch_bounds__(kSplitThreads) void q4_split_kernel(SplitArgs a) {
     __shared__ float sq[kSplitThreads / 64];
     const int tok = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     const float *x = a.x + (size_t)tok * a.cols;
+    for (int i = tok * kSplitThreads + tid; i < a.n_done; i += gridDim.x * kSplitThreads) a.done[i] = 0;
     constexpr int KEEP = 2;  // packets of 8 a thread keeps (16384 columns), the rest is read twice
     float keep[KEEP][8];
     uint32_t m = 0;
@@ -535,16 +571,21 @@ struct MmArgs {
     Q4Args q;
     const _Float16 *xp;
     const float *fac;
+    float *part;  // [row groups][KS][B][rows]
+    int *done;    // [row groups] workgroups counted, 0 before the launch
 };
 
 template <int NG, bool ZP, bool WIDE, int RT, int W, int DW>
-__global__ __launch_bounds__(64 * W) void q4mm_kernel(MmArgs ma) {
+__global__ __launch_bounds__(64 * W, 4) void q4mm_kernel(MmArgs ma) {
     const Q4Args &a = ma.q;
     constexpr int SPG = 4 / NG, PL = WIDE ? 2 : 1;
     __shared__ __align__(16) float red[W * RT * 256];  // [W][RT][16 columns][16 rows]
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int rt0 = blockIdx.x * RT;
+    // this workgroup's share of the blocks, and its waves' blocks k0 + wv, k0 + wv + W, ...
+    const int ks = blockIdx.y, KS = gridDim.y;
+    const int k0 = (int)((int64_t)a.kb_n * ks / KS), k1 = (int)((int64_t)a.kb_n * (ks + 1) / KS);
     const int n_rt = (a.rows + kRow - 1) / kRow;
     const uint8_t *sc_base = a.packed + (size_t)a.n_rec * 1024;
     const uint8_t *zp_base = sc_base + (size_t)a.n_rec * 32 * NG;
@@ -560,8 +601,8 @@ __global__ __launch_bounds__(64 * W) void q4mm_kernel(MmArgs ma) {
     for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     uint4 cw[DW][RT];
-    half4 cs[DW][RT][NG];
-    uint32_t cz[DW][RT][NG];
+    Scales<NG> cs[DW][RT];
+    uint32_t cz[DW][RT];
     half8 cx[4][PL];
     auto load_w = [&](int st, int kb) {
 #pragma unroll
@@ -570,12 +611,8 @@ __global__ __launch_bounds__(64 * W) void q4mm_kernel(MmArgs ma) {
             cw[st][t] = __builtin_bit_cast(
                 uint4, __builtin_nontemporal_load(
                            reinterpret_cast<const u32x4_t *>(a.packed + rec * 1024) + lane));
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                cs[st][t][i] =
-                    *reinterpret_cast<const half4 *>(sc_base + (rec * NG + i) * 32 + g * 8);
-                if (ZP) cz[st][t][i] = zp_base[(rec * NG + i) * 16 + n];
-            }
+            cs[st][t].load(sc_base + (rec * 16 + 4 * g + (n & 3)) * (2 * NG));
+            if (ZP) cz[st][t] = load_zeros<NG>(zp_base + (rec * 16 + n) * NG);
         }
     };
     auto load_x = [&](int w, int kb) {
@@ -583,20 +620,20 @@ __global__ __launch_bounds__(64 * W) void q4mm_kernel(MmArgs ma) {
 #pragma unroll
         for (int p = 0; p < PL; ++p) cx[w][p] = xp[p * 64];
     };
-    if (wv < a.kb_n) {
+    if (k0 + wv < k1) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) load_x(w, wv);
+        for (int w = 0; w < 4; ++w) load_x(w, k0 + wv);
     }
 #pragma unroll
     for (int d = 0; d < DW; ++d)
-        if (wv + d * W < a.kb_n) load_w(d, wv + d * W);
+        if (k0 + wv + d * W < k1) load_w(d, k0 + wv + d * W);
     auto blocks = [&](auto all, int kb0) {  // as in q4mv_kernel
         constexpr bool ALL = decltype(all)::value;
 #pragma unroll
         for (int u = 0; u < DW; ++u) {
             const int kb = kb0 + u * W;
-            if (!ALL && kb >= a.kb_n) break;
-            const int kx = kb + W < a.kb_n ? kb + W : kb;  // the last block's are loaded again
+            if (!ALL && kb >= k1) break;
+            const int kx = kb + W < k1 ? kb + W : kb;  // the last block's are loaded again
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 f32x4 z[RT];
@@ -608,7 +645,7 @@ __global__ __launch_bounds__(64 * W) void q4mm_kernel(MmArgs ma) {
                     for (int t = 0; t < RT; ++t) {
                         const uint4 q = cw[u][t];
                         const uint32_t word = w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w;
-                        const half8 aw = widen(word, bits, Offsets::of<ZP>(cz[u][t][i]));
+                        const half8 aw = widen(word, bits, Offsets::of<ZP>(cz[u][t] >> (8 * i)));
 #pragma unroll
                         for (int p = 0; p < PL; ++p)
                             z[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(aw, cx[w][p], z[t], 0, 0, 0);
@@ -619,27 +656,57 @@ __global__ __launch_bounds__(64 * W) void q4mm_kernel(MmArgs ma) {
                 for (int t = 0; t < RT; ++t)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        acc[t][j] = fmaf(z[t][j], (float)cs[u][t][i][j], acc[t][j]);
+                        acc[t][j] = fmaf(z[t][j], (float)cs[u][t](j, i), acc[t][j]);
             }
-            if (ALL || kb + DW * W < a.kb_n) load_w(u, kb + DW * W);
+            if (ALL || kb + DW * W < k1) load_w(u, kb + DW * W);
         }
     };
-    int kb0 = wv;
-    for (; kb0 + (2 * DW - 1) * W < a.kb_n; kb0 += DW * W) blocks(std::true_type{}, kb0);
-    for (; kb0 < a.kb_n; kb0 += DW * W) blocks(std::false_type{}, kb0);
+    int kb0 = k0 + wv;
+    for (; kb0 + (2 * DW - 1) * W < k1; kb0 += DW * W) blocks(std::true_type{}, kb0);
+    for (; kb0 < k1; kb0 += DW * W) blocks(std::false_type{}, kb0);
 #pragma unroll
     for (int t = 0; t < RT; ++t)
         *reinterpret_cast<f32x4 *>(red + ((wv * RT + t) * 16 + n) * 16 + 4 * g) = acc[t];
     __syncthreads();
-    for (int o = tid; o < RT * kRow * a.B; o += 64 * W) {
-        const int b = o / (RT * kRow), lr = o - b * (RT * kRow);
-        const int row = rt0 * kRow + lr;
-        if (row >= a.rows) continue;
-        float v = sum_waves<RT, W, !WIDE>(red, b, lr >> 4, lr & 15) * ma.fac[2 * b] * ma.fac[2 * b + 1];
+    constexpr int ROWS = RT * kRow;
+    auto finish = [&](int o, float v) {
+        const int b = o / ROWS, row = rt0 * kRow + o % ROWS;
+        if (row >= a.rows) return;
+        v *= ma.fac[2 * b] * ma.fac[2 * b + 1];
         if (a.bias) v += a.bias[row];
         const size_t at = (size_t)b * a.rows + row;
         if (a.resid) v += a.resid[at];
         a.y[at] = v;
+    };
+    const int n_out = ROWS * a.B;
+    if (KS == 1) {
+        for (int o = tid; o < n_out; o += 64 * W)
+            finish(o, sum_waves<RT, W, !WIDE>(red, o / ROWS, o % ROWS / 16, o % 16));
+        return;
+    }
+    // The workgroups of these rows leave their sums in the workspace, and the last one to come
+    // adds them up, in the order of their columns.  The sums are written and read as agent-scope
+    // atomics, which are coherent by themselves: each wave waits for its own stores, the barrier
+    // for the waves, and only then is the workgroup counted (no cache write-back is needed).
+    float *part = ma.part + (size_t)blockIdx.x * KS * n_out;
+    for (int o = tid; o < n_out; o += 64 * W)
+        __hip_atomic_store(part + (size_t)ks * n_out + o,
+                           sum_waves<RT, W, !WIDE>(red, o / ROWS, o % ROWS / 16, o % 16),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __builtin_amdgcn_s_waitcnt(0);
+    __shared__ int last;
+    __syncthreads();
+    if (tid == 0)
+        last = __hip_atomic_fetch_add(ma.done + blockIdx.x, 1, __ATOMIC_RELAXED,
+                                      __HIP_MEMORY_SCOPE_AGENT) == KS - 1;
+    __syncthreads();
+    if (!last) return;
+    for (int o = tid; o < n_out; o += 64 * W) {
+        float v = 0.0f;
+        for (int k = 0; k < KS; ++k)
+            v += __hip_atomic_load(part + (size_t)k * n_out + o, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+        finish(o, v);
     }
 }
 
@@ -650,40 +717,79 @@ hipError_t launch_q4mv_one(const Q4Args &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int NG, bool ZP, bool WIDE, int RT, int W, int DW>
-hipError_t launch_q4mm_one(const MmArgs &a, hipStream_t s) {
-    const int n_rt = (a.q.rows + kRow - 1) / kRow;
-    q4mm_kernel<NG, ZP, WIDE, RT, W, DW><<<(n_rt + RT - 1) / RT, 64 * W, 0, s>>>(a);
-    return hipGetLastError();
+// Rows of a workgroup of the product, and how often its columns are cut.  The
+// cuts make the number of workgroups fit the 256 compute units: G row groups cut
+// KS times take ceil(G KS / 256) rounds of 1 / KS of a row group's work each (one
+// workgroup per unit and round; several fit at a time, and the units share the
+// memory, so it is a matter of equal shares, not of waves left idle).  Few cuts
+// are preferred: each adds a sum to be written and read.  9216 x 8192, five
+// tokens: 20.5 us uncut, 18.6 cut in 3 or 4, 19.7 in 8, 23.9 in 16.
+// (four tiles a wave share one activation operand at B > 8, where that is 8 KiB a
+// block: 36864 x 12288 and sixteen tokens 71 us, with two tiles 83; at B <= 8 the
+// smaller shares of two tiles win, 18.6 against 19.5 us)
+constexpr int kMmWaves = 4;
+constexpr int mm_rt(int B) { return B > 8 ? 4 : 2; }
+
+struct MmShape {
+    int groups, cuts;
+};
+
+MmShape mm_shape(int rows, int cols, int B) {
+    const int kb_n = (cols + kBlk - 1) / kBlk;
+    const int per = kRow * mm_rt(B), g = (rows + per - 1) / per;
+    const int most = kb_n / kMmWaves < 1 ? 1 : kb_n / kMmWaves > 16 ? 16 : kb_n / kMmWaves;
+    int best = 1;
+    double cost = 0;
+    for (int ks = 1; ks <= most; ++ks) {
+        const int64_t wgs = (int64_t)g * ks;
+        const double c = (double)((wgs + 255) / 256) / ks + 0.04 * g / 256 * (ks - 1);
+        if (ks == 1 || c < cost) {
+            best = ks;
+            cost = c;
+        }
+    }
+    return {g, best};
 }
 
-size_t split_bytes(int cols, int B) {
-    return (size_t)((cols + kBlk - 1) / kBlk) * (B > 8 ? 8192 : 4096);
-}
+// Workspace of B > 2: the split activations, two factors a token, the counters
+// and, where the columns are cut, the sums.
+struct MmWs {
+    size_t fac, done, part, total;
+};
 
-MmArgs split_args(const Q4Args &a, void *ws) {
-    return MmArgs{a, static_cast<const _Float16 *>(ws),
-                  reinterpret_cast<const float *>(static_cast<const uint8_t *>(ws) +
-                                                  split_bytes(a.cols, a.B))};
-}
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-hipError_t launch_q4_split(const Q4Args &a, void *ws, hipStream_t s) {
-    SplitArgs sa{a.x, static_cast<_Float16 *>(ws),
-                 reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + split_bytes(a.cols, a.B)),
-                 a.cols, a.kb_n, a.B > 8, a.eps};
-    q4_split_kernel<<<a.B, kSplitThreads, 0, s>>>(sa);
-    return hipGetLastError();
+MmWs mm_ws(int rows, int cols, int B) {
+    const MmShape sh = mm_shape(rows, cols, B);
+    MmWs w;
+    w.fac = (size_t)((cols + kBlk - 1) / kBlk) * (B > 8 ? 8192 : 4096);
+    w.done = w.fac + 256;
+    w.part = w.done + up256((size_t)sh.groups * 4);
+    w.total = w.part + (sh.cuts > 1 ? (size_t)sh.groups * sh.cuts * B * mm_rt(B) * kRow * 4 : 0);
+    return w;
 }
 
 template <int NG, bool ZP>
 hipError_t launch_q4_shape(const Q4Args &a, void *ws, hipStream_t s) {
     if (a.B == 1) return launch_q4mv_one<NG, ZP, 1, 1, 8, 2>(a, s);
     if (a.B == 2) return launch_q4mv_one<NG, ZP, 2, 1, 8, 2>(a, s);
-    hipError_t e = launch_q4_split(a, ws, s);
+    const MmShape sh = mm_shape(a.rows, a.cols, a.B);
+    const MmWs w = mm_ws(a.rows, a.cols, a.B);
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    _Float16 *xp = reinterpret_cast<_Float16 *>(base);
+    float *fac = reinterpret_cast<float *>(base + w.fac);
+    int *done = reinterpret_cast<int *>(base + w.done);
+    q4_split_kernel<<<a.B, kSplitThreads, 0, s>>>(
+        SplitArgs{a.x, xp, fac, a.cols, a.kb_n, a.B > 8, a.eps, done, sh.cuts > 1 ? sh.groups : 0});
+    hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const MmArgs m = split_args(a, ws);
-    if (a.B <= 8) return launch_q4mm_one<NG, ZP, false, 2, 4, 2>(m, s);
-    return launch_q4mm_one<NG, ZP, true, 4, 4, 2>(m, s);
+    const MmArgs m{a, xp, fac, reinterpret_cast<float *>(base + w.part), done};
+    const dim3 grid(sh.groups, sh.cuts);
+    if (a.B <= 8)
+        q4mm_kernel<NG, ZP, false, mm_rt(8), kMmWaves, 1><<<grid, 64 * kMmWaves, 0, s>>>(m);
+    else
+        q4mm_kernel<NG, ZP, true, mm_rt(16), kMmWaves, 1><<<grid, 64 * kMmWaves, 0, s>>>(m);
+    return hipGetLastError();
 }
 
 int64_t q4_records(int rows, int cols) {
@@ -704,7 +810,7 @@ hipError_t launch_q4_pack(const uint8_t *codes, const uint16_t *scales, const ui
     return hipGetLastError();
 }
 
-size_t q4_ws_bytes(int cols, int B) { return B <= 2 ? 0 : split_bytes(cols, B) + 256; }
+size_t q4_ws_bytes(int rows, int cols, int B) { return B <= 2 ? 0 : mm_ws(rows, cols, B).total; }
 
 hipError_t launch_q4_matvec(const uint8_t *packed, int rows, int cols, int group, bool zeros,
                             const float *x, int B, float eps, const float *bias,
