@@ -182,40 +182,67 @@ hipError_t launch_block_tables(const int32_t *lens, const int32_t *adds, int R, 
 }
 
 // ---------------------------------------------------------------------------
-// Append.  Each workgroup takes 16 tokens of one head, keys or values.
-//   keys:   a thread converts one packet (E head dimensions of a token) and
-//           stores it with one 16-byte store, tokens fastest, so that tokens of
-//           neighbouring slots write neighbouring packets;
-//   values: a packet is E neighbouring slots of one dimension.  Tokens whose
-//           slots run on inside a packet are written together: the first of
-//           the run (its packet's first slot, or one whose predecessor in the
-//           input is not the slot before) takes all of it, each lane one
-//           dimension, a whole packet as one 16-byte store and a part of one
-//           element by element.  A decode step's tokens are runs of one.
+// Append.  Each workgroup takes T (16 or 64) tokens of one head, keys or values.
+//   keys:   rows are read along the dimensions, rounded into LDS and stored from
+//           there a packet (E dimensions of a token) per thread, tokens fastest:
+//           neighbouring slots write neighbouring packets, so that both sides
+//           move whole cache lines;
+//   values: a packet is E neighbouring slots of one dimension.  Where E tokens of
+//           the input run through a whole packet, the workgroup that has the
+//           first of them writes it, a thread per dimension and one 16-byte
+//           store; the tokens of broken packets (a decode step's are, most of
+//           them) are stored element by element.
 // HBM bounds long inputs (each element is read once and written once), the
 // launch short ones.  The conversion is one rounding: fp16 to nearest, fp8 the
 // nearest E4M3 value of x / scale (an fp32 division), saturating at +-448 (NaN
 // stays NaN).
 // ---------------------------------------------------------------------------
-constexpr int kAppTokens = 16;
-
 struct AppArgs {
     const void *k, *v;
     uint8_t *kc, *vc;
     const float *ks, *vs;
     const int32_t *slots;
     int64_t ldk, ldv;
-    int N, H, D, shift;
+    int N, H, shift;
     int64_t n_slots;
 };
 
-__device__ __forceinline__ float e4m3_clamp(float v) {
-    return v > 448.0f ? 448.0f : v < -448.0f ? -448.0f : v;  // NaN passes
-}
+// x / s, correctly rounded, for one s and many x: with y the rounded reciprocal,
+// q = x y is within two steps, and each q + (x - q s) y, the rest taken exactly,
+// comes within the last rounding.  Quotients past E4M3's range need no more than
+// their size.  Scales so small or large that y or the rest leaves the normal
+// range are divided by as they are.
+struct Quotient {
+    float s, y;
+    bool plain;
+    __device__ __forceinline__ explicit Quotient(float scale) : s(scale), y(1.0f / scale) {
+        plain = !(fabsf(scale) > 1e-18f && fabsf(scale) < 1e18f);
+    }
+    __device__ __forceinline__ float operator()(float x) const {
+        if (plain) return x / s;
+        float q = x * y;
+        const float q1 = fmaf(fmaf(-q, s, x), y, q);
+        const float q2 = fmaf(fmaf(-q1, s, x), y, q1);
+        return fabsf(q) < 1024.0f ? q2 : q;  // (infinities and NaN too)
+    }
+};
 
+// Four values as E4M3, saturating; NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_clamp(a), e4m3_clamp(b), 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(e4m3_clamp(c), e4m3_clamp(d), w, true);
+    const float sum = (a + b) + (c + d);
+    if (!(fabsf(sum) < __builtin_inff())) {  // rare: some value may be NaN
+        a = a > 448.0f ? 448.0f : a < -448.0f ? -448.0f : a;
+        b = b > 448.0f ? 448.0f : b < -448.0f ? -448.0f : b;
+        c = c > 448.0f ? 448.0f : c < -448.0f ? -448.0f : c;
+        d = d > 448.0f ? 448.0f : d < -448.0f ? -448.0f : d;
+    } else {
+        a = __builtin_amdgcn_fmed3f(a, -448.0f, 448.0f);
+        b = __builtin_amdgcn_fmed3f(b, -448.0f, 448.0f);
+        c = __builtin_amdgcn_fmed3f(c, -448.0f, 448.0f);
+        d = __builtin_amdgcn_fmed3f(d, -448.0f, 448.0f);
+    }
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
 
 // E fp32 values as one packet.
@@ -232,102 +259,163 @@ __device__ __forceinline__ uint4 to_packet(const float *v) {
     }
 }
 
-template <bool FP8, bool SRC16>
+// Four source elements from p on, as fp32.
+template <bool SRC16>
+__device__ __forceinline__ float4 four(const void *base, size_t at) {
+    if constexpr (SRC16) {
+        typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+        const half4 x = *reinterpret_cast<const half4 *>(static_cast<const _Float16 *>(base) + at);
+        return make_float4((float)x[0], (float)x[1], (float)x[2], (float)x[3]);
+    } else {
+        return *reinterpret_cast<const float4 *>(static_cast<const float *>(base) + at);
+    }
+}
+
+template <bool FP8, bool SRC16, int D, int T>
 __global__ __launch_bounds__(256) void kv_append_kernel(AppArgs a) {
-    constexpr int E = FP8 ? 16 : 8;
+    constexpr int E = FP8 ? 16 : 8, ES = FP8 ? 1 : 2;
     typedef typename std::conditional<SRC16, _Float16, float>::type S;
-    const int n0 = blockIdx.x * kAppTokens, h = blockIdx.y;
+    const int n0 = blockIdx.x * T, h = blockIdx.y, tid = threadIdx.x;
     const int ps = 1 << a.shift;
+    auto slot_of = [&](int n) {
+        const int s = n >= 0 && n < a.N ? a.slots[n] : -1;
+        return s < a.n_slots ? s : -1;
+    };
     if (blockIdx.z == 0) {
-        const float ks = FP8 ? a.ks[h] : 1.0f;
-        const int npk = a.D / E;
-        for (int i = threadIdx.x; i < npk * kAppTokens; i += 256) {
-            const int n = n0 + (i & (kAppTokens - 1)), pk = i / kAppTokens;
-            if (n >= a.N) continue;
-            const int slot = a.slots[n];
-            if (slot < 0 || slot >= a.n_slots) continue;
-            const S *src = static_cast<const S *>(a.k) + (size_t)n * a.ldk + (size_t)h * a.D + pk * E;
-            float v[E];
-            if constexpr (SRC16) {
+        constexpr int pitch = D * ES + 16, Q = D / 4, PER = (T * Q + 255) / 256, npk = D / E;
+        __shared__ __align__(16) uint8_t tile[T * pitch];
+        const int t = tid % T, slot = slot_of(n0 + t);
+        float4 x[PER];
 #pragma unroll
-                for (int q = 0; q < E / 8; ++q) {
-                    const half8 x = reinterpret_cast<const half8 *>(src)[q];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[8 * q + e] = (float)x[e];
-                }
-            } else {
-#pragma unroll
-                for (int q = 0; q < E / 4; ++q) {
-                    const float4 x = reinterpret_cast<const float4 *>(src)[q];
-                    v[4 * q] = x.x;
-                    v[4 * q + 1] = x.y;
-                    v[4 * q + 2] = x.z;
-                    v[4 * q + 3] = x.w;
-                }
-            }
-            if (FP8) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) v[e] = v[e] / ks;
-            }
-            const size_t page = (size_t)(slot >> a.shift), o = (size_t)(slot & (ps - 1));
-            const size_t at = ((page * a.H + h) * npk + pk) * ps + o;
-            reinterpret_cast<uint4 *>(a.kc)[at] = to_packet<FP8>(v);
+        for (int k = 0; k < PER; ++k) {
+            const int i = tid + 256 * k, n = n0 + i / Q;
+            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < T * Q && n < a.N)
+                x[k] = four<SRC16>(a.k, (size_t)n * a.ldk + (size_t)h * D + 4 * (i % Q));
         }
+        const Quotient by(FP8 ? a.ks[h] : 1.0f);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int i = tid + 256 * k;
+            uint8_t *to = tile + i / Q * pitch + 4 * (i % Q) * ES;
+            if (i >= T * Q) break;
+            if constexpr (FP8) {
+                *reinterpret_cast<uint32_t *>(to) = e4m3x4(by(x[k].x), by(x[k].y), by(x[k].z), by(x[k].w));
+            } else {
+                typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+                *reinterpret_cast<half4 *>(to) = half4{(_Float16)x[k].x, (_Float16)x[k].y,
+                                                       (_Float16)x[k].z, (_Float16)x[k].w};
+            }
+        }
+        __syncthreads();
+        if (slot < 0) return;
+        const size_t page = (size_t)(slot >> a.shift), o = (size_t)(slot & (ps - 1));
+        uint4 *dst = reinterpret_cast<uint4 *>(a.kc) + (page * a.H + h) * npk * ps + o;
+        for (int pk = tid / T; pk < npk; pk += 256 / T)
+            dst[(size_t)pk * ps] = *reinterpret_cast<const uint4 *>(tile + t * pitch + pk * 16);
         return;
     }
-    const float vs = FP8 ? a.vs[h] : 1.0f;
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    for (int t = 0; t < kAppTokens / 4; ++t) {
-        const int n = n0 + wv * (kAppTokens / 4) + t;
-        if (n >= a.N) break;
-        const int slot = a.slots[n];
-        if (slot < 0 || slot >= a.n_slots) continue;
-        const int o = slot & (E - 1);
-        if (o != 0 && n > 0 && a.slots[n - 1] == slot - 1) continue;  // inside a run
-        bool runs = false;
-        if (lane < E - o && n + lane < a.N) runs = a.slots[n + lane] == slot + lane;
-        const int m = __ffsll((long long)~__ballot(runs)) - 1;  // >= 1: lane 0 is the slot itself
-        const size_t page = (size_t)(slot >> a.shift);
-        const size_t row = (page * a.H + h) * (size_t)(ps / E) + ((slot & (ps - 1)) / E);
-        for (int d = lane; d < a.D; d += 64) {
-            const S *src = static_cast<const S *>(a.v) + (size_t)n * a.ldv + (size_t)h * a.D + d;
-            float v[E];
+    // slots from E - 1 before the first token on (a packet may have begun there)
+    __shared__ int near[T + 2 * (E - 1)];
+    __shared__ uint64_t whole_s, lead_s;
+    for (int i = tid; i < T + 2 * (E - 1); i += 256) near[i] = slot_of(n0 - (E - 1) + i);
+    __syncthreads();
+    if (tid < 64) {  // which tokens belong to a whole packet, and which begin one
+        bool all = false, lead = false;
+        if (tid < T) {
+            const int slot = near[tid + E - 1], o = slot & (E - 1);
+            all = slot >= 0;
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                v[e] = e < m ? (float)src[(size_t)e * a.ldv] : 0.0f;
-                if (FP8) v[e] = v[e] / vs;
-            }
-            const uint4 pkt = to_packet<FP8>(v);
-            uint8_t *dst = a.vc + (row * a.D + d) * 16;
-            if (m == E) {
-                *reinterpret_cast<uint4 *>(dst) = pkt;
-            } else {
-                const uint32_t w[4] = {pkt.x, pkt.y, pkt.z, pkt.w};
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    if (e >= m) continue;
-                    if constexpr (FP8) dst[o + e] = (uint8_t)(w[e / 4] >> (8 * (e % 4)));
-                    else reinterpret_cast<uint16_t *>(dst)[o + e] =
-                            (uint16_t)(w[e / 2] >> (16 * (e % 2)));
-                }
-            }
+            for (int e = 0; e < E; ++e) all = all && near[(tid + E - 1) - o + e] == slot - o + e;
+            lead = all && o == 0;
         }
+        const uint64_t w = __ballot(all), l = __ballot(lead);
+        if (tid == 0) {
+            whole_s = w;
+            lead_s = l;
+        }
+    }
+    __syncthreads();
+    const uint64_t whole = whole_s, leads = lead_s;
+    const int n_lead = __popcll(leads);
+    const Quotient by(FP8 ? a.vs[h] : 1.0f);
+    const S *src = static_cast<const S *>(a.v) + (size_t)h * D;
+    auto packet_at = [&](int slot, int d) {  // bytes
+        const size_t row = ((size_t)(slot >> a.shift) * a.H + h) * (size_t)(ps / E) + ((slot & (ps - 1)) / E);
+        return a.vc + (row * D + d) * 16;
+    };
+    if (n_lead) {
+        constexpr int PER = (T / E * D + 255) / 256;  // packets of a thread: whole ones are E apart
+        float v[PER][E];
+        int slot[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int i = tid + 256 * k, p = i / D, d = i % D;
+            slot[k] = -1;
+            if (p >= n_lead) continue;
+            uint64_t m = leads;
+            for (int x = 0; x < p; ++x) m &= m - 1;
+            const int t = __ffsll((long long)m) - 1;
+            slot[k] = near[t + E - 1];
+            const S *from = src + (size_t)(n0 + t) * a.ldv + d;
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[k][e] = (float)from[(size_t)e * a.ldv];
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            if (slot[k] < 0) continue;
+            if (FP8) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[k][e] = by(v[k][e]);
+            }
+            *reinterpret_cast<uint4 *>(packet_at(slot[k], (tid + 256 * k) % D)) = to_packet<FP8>(v[k]);
+        }
+    }
+    // the other tokens, by elements
+    if (whole == ~0ull >> (64 - T)) return;
+#pragma unroll 4
+    for (int i = tid; i < T * D; i += 256) {
+        const int t = i / D, d = i % D, slot = near[t + E - 1];
+        if (slot < 0 || ((whole >> t) & 1)) continue;
+        const float v = (float)src[(size_t)(n0 + t) * a.ldv + d];
+        uint8_t *dst = packet_at(slot, d) + (slot & (E - 1)) * ES;
+        if constexpr (FP8) *dst = (uint8_t)e4m3x4(by(v), 0.0f, 0.0f, 0.0f);
+        else *reinterpret_cast<_Float16 *>(dst) = (_Float16)v;
+    }
+}
+
+template <int D, int T>
+hipError_t launch_append_dim(const KvCache &c, const AppArgs &a, bool src16, hipStream_t s) {
+    const dim3 grid((a.N + T - 1) / T, c.H, 2);
+    if (c.fp8) {
+        if (src16) kv_append_kernel<true, true, D, T><<<grid, 256, 0, s>>>(a);
+        else kv_append_kernel<true, false, D, T><<<grid, 256, 0, s>>>(a);
+    } else {
+        if (src16) kv_append_kernel<false, true, D, T><<<grid, 256, 0, s>>>(a);
+        else kv_append_kernel<false, false, D, T><<<grid, 256, 0, s>>>(a);
+    }
+    return hipGetLastError();
+}
+
+template <int T>
+hipError_t launch_append(const KvCache &c, const AppArgs &a, bool src16, hipStream_t s) {
+    switch (c.D) {
+        case 64: return launch_append_dim<64, T>(c, a, src16, s);
+        case 96: return launch_append_dim<96, T>(c, a, src16, s);
+        case 128: return launch_append_dim<128, T>(c, a, src16, s);
+        default: return launch_append_dim<256, T>(c, a, src16, s);
     }
 }
 
 hipError_t launch_kv_append(const KvCache &c, const void *k, const void *v, bool src16, int64_t ldk,
                             int64_t ldv, const int32_t *slots, int N, hipStream_t s) {
-    AppArgs a{k, v, c.k, c.v, c.ks, c.vs, slots, ldk, ldv, N, c.H, c.D, c.shift,
-              (int64_t)c.pages << c.shift};
-    const dim3 grid((N + kAppTokens - 1) / kAppTokens, c.H, 2);
-    if (c.fp8) {
-        if (src16) kv_append_kernel<true, true><<<grid, 256, 0, s>>>(a);
-        else kv_append_kernel<true, false><<<grid, 256, 0, s>>>(a);
-    } else {
-        if (src16) kv_append_kernel<false, true><<<grid, 256, 0, s>>>(a);
-        else kv_append_kernel<false, false><<<grid, 256, 0, s>>>(a);
-    }
-    return hipGetLastError();
+    const AppArgs a{k, v, c.k, c.v, c.ks, c.vs, slots, ldk, ldv, N, c.H, c.shift,
+                    (int64_t)c.pages << c.shift};
+    // A workgroup is a chain of waits (slots, rows, stores) whatever it moves, so it moves as
+    // much as fits its registers once the chip is full of them (8191 tokens of 8 heads to fp8,
+    // 84 MB: 24 us, with 16 tokens a workgroup 38 us); a step's few tokens spread over more.
+    const bool many = (int64_t)N * c.H * 2 >= (int64_t)64 * 512;
+    return many ? launch_append<64>(c, a, src16, s) : launch_append<16>(c, a, src16, s);
 }
 
 }  // namespace spffn

@@ -188,14 +188,47 @@ def test_append_extremes(dtype):
     check_append(dtype, torch.float32, 2, 64, 16, 4, list(range(40)), True, 6, big=True)
 
 
+def test_append_quotients_at_the_borders():
+    # every E4M3 border (the value half way between two neighbours) and its fp32 neighbours,
+    # times scales of all sizes: the quotient decides the code, so it has to be exact
+    codes = torch.arange(0, 0x7E, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    nxt = torch.arange(1, 0x7F, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    g = torch.Generator().manual_seed(9)
+    H, D, page = 8, 64, 16
+    scales = torch.tensor([1.0, 0.1, 3.7e-5, 7.0, 1e-20, 3e19, 0.3333333, 1.7e6])
+    rows = []
+    for h in range(H):
+        x = (codes + nxt) / 2 * scales[h]
+        ulp = x.abs() * 2.0 ** -23
+        x = torch.cat([x, x + ulp, x - ulp, -x, x + 2 * ulp, x - 2 * ulp,
+                       torch.randn(5 * 126, generator=g) * scales[h] * 100])
+        rows.append(x[:21 * D].view(21, D) if x.numel() >= 21 * D else
+                    torch.cat([x, x.new_zeros(21 * D - x.numel())]).view(21, D))
+    new = torch.stack(rows, 1).contiguous()
+    k = torch.zeros(2, H, D // 16, page, 16).to(torch.float8_e4m3fn).to(DEV)
+    v = torch.zeros(2, H, page // 16, D, 16).to(torch.float8_e4m3fn).to(DEV)
+    cache = spffn.KVCache(k, v, scales.to(DEV), scales.to(DEV))
+    spffn.kv_append(cache, new.to(DEV), new.to(DEV), i32(list(range(21))))
+    torch.cuda.synchronize()
+    want = ref.round_rows(new, torch.float8_e4m3fn, scales).view(torch.uint8)
+    assert torch.equal(ref.rows_of_k(k.cpu())[:21].view(torch.uint8), want)
+    assert torch.equal(ref.rows_of_v(v.cpu())[:21].view(torch.uint8), want)
+
+
 @pytest.mark.parametrize("dtype", CACHE)
-def test_append_prompt(dtype):
+@pytest.mark.parametrize("src", [torch.float32, torch.float16])
+@pytest.mark.parametrize("H,D,start", [(2, 128, 7), (9, 128, 7), (8, 64, 16), (8, 96, 0), (9, 256, 9)])
+def test_append_prompt(dtype, src, H, D, start):
+    # 2001 tokens of two heads go in small workgroups, those of eight in large ones
     page, pages = 32, 70
     order = list(range(pages))
     random.Random(3).shuffle(order)
-    slots = [order[(i + 7) // page] * page + (i + 7) % page for i in range(2001)]
+    at = lambda i: order[(i + start) // page] * page + (i + start) % page  # noqa: E731
+    slots = [at(i) for i in range(2101)]
     slots[100] = -1
-    check_append(dtype, torch.float32, 2, 128, page, pages, slots, True, 7)
+    slots[640:660] = [at(i) for i in range(659, 639, -1)]  # backwards: no packet is whole
+    slots[1203], slots[1209] = slots[1209], slots[1203]
+    check_append(dtype, src, H, D, page, pages, slots, True, 7)
 
 
 def test_append_far_offsets():
