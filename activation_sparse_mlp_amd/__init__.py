@@ -11,7 +11,7 @@ from ._lib import (DECODE_DENSE, F16, F32, MAX_BATCH, PERMUTED_KEYS, Q4_0, RELU,
                    q4_0_repack, threshold, version, set_wait_limit, WAIT_LIMIT_DEFAULT,
                    stream_read, workspace_clear_status, workspace_status,
                    decode_step_noalloc, decode_step_adaptive, tau_threshold,
-                   KVCache, MAX_NEW, MAX_REQUESTS, Q4Matrix, block_tables, kv_append, q4_matvec,
-                   tree_attention)
+                   Attention, KVCache, MAX_NEW, MAX_REQUESTS, Q4Matrix, attn_step, block_tables,
+                   kv_append, q4_matvec, tree_attention)
 
 LIB_PATH = __import__("os").path.join(__import__("os").path.dirname(__file__), "libspffn.so")

@@ -49,6 +49,12 @@ class CacheDesc(C.Structure):
                 ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("dtype", C.c_int32)]
 
 
+class AttnDesc(C.Structure):
+    _fields_ = [("qkv", Q4Desc), ("out", Q4Desc), ("qkv_bias", C.c_void_p),
+                ("out_bias", C.c_void_p), ("heads", C.c_int32), ("rms_eps", C.c_float),
+                ("scale", C.c_float)]
+
+
 class Trace(C.Structure):
     _fields_ = [("h_in", C.c_void_p), ("union_mask", C.c_void_p), ("logits", C.c_void_p),
                 ("events", C.c_void_p)]
@@ -95,6 +101,9 @@ SIGNATURES = {
     "spffn_tree_attention_workspace_bytes": (_sz, [_vp, _i32, _i32, _i32]),
     "spffn_tree_attention": (_i32, [_vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp, _i32, _i32,
                                     _vp, _i32, _f32, _vp, _i64, _vp, _sz, _vp]),
+    "spffn_attn_workspace_bytes": (_sz, [_vp, _vp, _i32, _i32]),
+    "spffn_attn_step": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _i32,
+                               _vp, _sz, _vp]),
     "spffn_stream_read": (_i32, [_vp, _i64, _vp, _vp]),
     "spffn_set_wait_limit": (_i32, [_i32]),
     "spffn_last_error": (C.c_char_p, []),
@@ -903,6 +912,71 @@ def tree_attention(cache, q, starts, lens, table, mask=None, scale=None, max_new
               heads, p_starts, p_lens, p_table, R, width, p_mask, max_new,
               dim ** -0.5 if scale is None else scale, out.data_ptr(), ld_out, pw, nb)
     return out
+
+
+class Attention:
+    """The attention of one layer: qkv, a Q4Matrix [(heads + 2 kv_heads) * head_dim,
+    d] (queries, keys, values), out, a Q4Matrix [d, heads * head_dim], fp32 biases
+    of their rows or None.  scale defaults to head_dim ** -0.5."""
+
+    def __init__(self, qkv, out, heads, head_dim, qkv_bias=None, out_bias=None, rms_eps=1e-5,
+                 scale=None):
+        if out.cols != heads * head_dim or out.rows != qkv.cols or qkv.rows <= out.cols or \
+                (qkv.rows - out.cols) % (2 * head_dim):
+            raise ValueError(f"qkv [{qkv.rows}, {qkv.cols}] and out [{out.rows}, {out.cols}] do not "
+                             f"fit {heads} heads of {head_dim}")
+        if out._index != qkv._index:
+            raise ValueError(f"qkv is on {qkv.device}, out on {out.device}")
+        _sizes((qkv_bias, qkv.rows, "qkv_bias"), (out_bias, out.rows, "out_bias"))
+        self.qkv, self.out, self.qkv_bias, self.out_bias = qkv, out, qkv_bias, out_bias
+        self.heads, self.head_dim, self.d, self._index = heads, head_dim, qkv.cols, qkv._index
+        self.kv_heads = (qkv.rows - out.cols) // (2 * head_dim)
+        self.desc = AttnDesc(
+            qkv=qkv.desc, out=out.desc, heads=heads, rms_eps=float(rms_eps),
+            qkv_bias=_maybe(qkv_bias, torch.float32, qkv.rows, self._index, "qkv_bias"),
+            out_bias=_maybe(out_bias, torch.float32, out.rows, self._index, "out_bias"),
+            scale=head_dim ** -0.5 if scale is None else float(scale))
+        self._ref = C.addressof(self.desc)
+
+    def workspace(self, cache, B, max_new):
+        """A workspace for attn_step of B tokens, up to max_new of one request."""
+        n = int(load().spffn_attn_workspace_bytes(self._ref, cache._ref, B, max_new))
+        if n == 0:
+            raise SpffnError(-2, "attn_workspace_bytes", load().spffn_last_error().decode())
+        return torch.empty(n, dtype=torch.uint8, device=self.qkv.device)
+
+
+def attn_step(attn, cache, x, starts, lens, slots, table, mask=None, max_new=None, h=None, ws=None):
+    """The attention half of a layer on the residual stream: h [B, d] = x + W_out
+    attention(W_qkv rms(x)), the new keys and values written to slots int32 [B] of
+    the cache.  starts, lens, table, mask, max_new as tree_attention; block_tables
+    makes starts and slots.  The layer's FFN follows with decode_step of a
+    one-layer model.  Tokens that no request names get the attention zero.  h may
+    be x (in place)."""
+    B, index, i32, f32 = _tokens(x, attn.d), attn._index, torch.int32, torch.float32
+    if cache.kv_heads != attn.kv_heads or cache.head_dim != attn.head_dim:
+        raise ValueError(f"the cache holds {cache.kv_heads} heads of {cache.head_dim}, the layer "
+                         f"has {attn.kv_heads} of {attn.head_dim}")
+    if cache._index != index:
+        raise ValueError(f"the cache is on {cache.device}, the layer on cuda:{index}")
+    R = lens.numel()
+    _sizes((starts, R + 1, "starts"), (slots, B, "slots"), (mask, B, "mask"),
+           (h, B * attn.d, "h"))
+    if table.dim() != 2 or table.shape[0] != R:
+        raise ValueError(f"table must have shape [{R}, width], got {tuple(table.shape)}")
+    max_new = B if max_new is None else int(max_new)
+    px = _plain(x, f32, B * attn.d, index, "x")
+    if h is None:
+        h = torch.empty_like(x)
+    if ws is None:
+        ws = attn.workspace(cache, B, max_new)
+    pw, nb = _work(ws, 256, index)
+    _call(index, "spffn_attn_step", attn._ref, cache._ref, px, _plain(h, f32, B * attn.d, index, "h"),
+          B, _plain(slots, i32, B, index, "slots"), _plain(starts, i32, R + 1, index, "starts"),
+          _plain(lens, i32, R, index, "lens"),
+          _plain(table, i32, R * table.shape[1], index, "table"), R, table.shape[1],
+          _maybe(mask, torch.int64, B, index, "mask"), max_new, pw, nb)
+    return h
 
 
 STREAM_SINK_WORDS = 4096

@@ -1005,48 +1005,159 @@ size_t spffn_tree_attention_workspace_bytes(const spffn_kv_cache *cache, int32_t
     return attn_ws_bytes(heads, c.H, c.D, max_new, dtype == SPFFN_F16);
 }
 
-spffn_status spffn_tree_attention(const spffn_kv_cache *cache, const void *q, int32_t dtype,
-                                  int64_t ld_q, int32_t N, int32_t heads, const int32_t *starts,
-                                  const int32_t *lens, const int32_t *table, int32_t R,
-                                  int32_t width, const int64_t *mask, int32_t max_new, float scale,
-                                  void *out, int64_t ld_out, void *ws, size_t ws_bytes,
-                                  void *stream) {
-    const char *who = "tree_attention";
+namespace {
+
+// spffn_tree_attention; with `clear`, zeros in the rows that no request names.
+spffn_status attend(const char *who, bool clear, const spffn_kv_cache *cache, const void *q,
+                    int32_t dtype, int64_t ld_q, int32_t N, int32_t heads, const int32_t *starts,
+                    const int32_t *lens, const int32_t *table, int32_t R, int32_t width,
+                    const int64_t *mask, int32_t max_new, float scale, void *out, int64_t ld_out,
+                    void *ws, size_t ws_bytes, void *stream) {
     KvCache c;
     if (spffn_status st = check_cache(who, cache, c)) return st;
     if (dtype != SPFFN_F32 && dtype != SPFFN_F16)
-        return fail(SPFFN_E_DTYPE, "tree_attention: queries of dtype %d (F32 or F16)", dtype);
+        return fail(SPFFN_E_DTYPE, "%s: queries of dtype %d (F32 or F16)", who, dtype);
     if (heads < 1 || heads > 65535 || heads % c.H)
-        return fail(SPFFN_E_SHAPE, "tree_attention: heads=%d is no multiple of kv_heads=%d", heads,
+        return fail(SPFFN_E_SHAPE, "%s: heads=%d is no multiple of kv_heads=%d", who, heads,
                     c.H);
     if (max_new < 1 || max_new > 64)
-        return fail(SPFFN_E_SHAPE, "tree_attention: max_new=%d outside [1, 64]", max_new);
+        return fail(SPFFN_E_SHAPE, "%s: max_new=%d outside [1, 64]", who, max_new);
     if (R < 1 || R > SPFFN_MAX_REQUESTS || width < 1 || N < 0)
-        return fail(SPFFN_E_SHAPE, "tree_attention: R=%d (1..%d), width=%d, N=%d", R,
+        return fail(SPFFN_E_SHAPE, "%s: R=%d (1..%d), width=%d, N=%d", who, R,
                     SPFFN_MAX_REQUESTS, width, N);
     // a request's work is counted in 32 bits on the device
     const int64_t steps = (((int64_t)width << c.shift) + 31) / 32 * heads * max_new;
     if (steps >= (int64_t)1 << 31)
-        return fail(SPFFN_E_SHAPE, "tree_attention: width=%d pages of %d tokens are too many", width,
+        return fail(SPFFN_E_SHAPE, "%s: width=%d pages of %d tokens are too many", who, width,
                     cache->page_size);
     if (!(scale == scale) || std::isinf(scale))
-        return fail(SPFFN_E_ARG, "tree_attention: scale must be finite");
+        return fail(SPFFN_E_ARG, "%s: scale must be finite", who);
     if (N == 0) return SPFFN_OK;
     const int64_t row = (int64_t)heads * c.D;
     if (spffn_status st = check_rows(who, "q", q, dtype, ld_q, row)) return st;
     if (spffn_status st = check_rows(who, "out", out, dtype, ld_out, row)) return st;
     const int es = dtype == SPFFN_F16 ? 2 : 4;
     if (overlap(q, ((size_t)(N - 1) * ld_q + row) * es, out, ((size_t)(N - 1) * ld_out + row) * es))
-        return fail(SPFFN_E_ARG, "tree_attention: q and out overlap");
+        return fail(SPFFN_E_ARG, "%s: q and out overlap", who);
     if (!starts || !lens || !table || !aligned(starts, 4) || !aligned(lens, 4) ||
         !aligned(table, 4) || !aligned(mask, 8))
-        return fail(SPFFN_E_ARG, "tree_attention: NULL or misaligned starts, lens, table or mask");
+        return fail(SPFFN_E_ARG, "%s: NULL or misaligned starts, lens, table or mask", who);
     const size_t need = attn_ws_bytes(heads, c.H, c.D, max_new, dtype == SPFFN_F16);
     if (spffn_status st = check_ws(need, ws, ws_bytes)) return st;
     AttnCall a{q, out, dtype == SPFFN_F16, ld_q, ld_out, N, heads, starts, lens, table,
-               R, width, max_new, mask, scale};
+               R, width, max_new, mask, scale, clear};
     SPFFN_HIP(launch_tree_attention(c, a, ws, (hipStream_t)stream), "attention launch");
     return SPFFN_OK;
+}
+
+}  // namespace
+
+spffn_status spffn_tree_attention(const spffn_kv_cache *cache, const void *q, int32_t dtype,
+                                  int64_t ld_q, int32_t N, int32_t heads, const int32_t *starts,
+                                  const int32_t *lens, const int32_t *table, int32_t R,
+                                  int32_t width, const int64_t *mask, int32_t max_new, float scale,
+                                  void *out, int64_t ld_out, void *ws, size_t ws_bytes,
+                                  void *stream) {
+    return attend("tree_attention", false, cache, q, dtype, ld_q, N, heads, starts, lens, table, R,
+                  width, mask, max_new, scale, out, ld_out, ws, ws_bytes, stream);
+}
+
+namespace {
+
+// Workspace of spffn_attn_step: the projections' output, the attention's, and
+// what the calls themselves need (one after the other, so the largest).
+struct AttnWs {
+    size_t qkv, att, call, total;
+    int64_t n_qkv;
+};
+
+spffn_status attn_sizes(const spffn_attn_desc *a, const spffn_kv_cache *cache, int32_t B,
+                        int32_t max_new, KvCache &c, AttnWs &w) {
+    if (!a) return fail(SPFFN_E_ARG, "attn_step: NULL description");
+    if (spffn_status st = check_cache("attn_step", cache, c)) return st;
+    if (spffn_status st = check_batch(B)) return st;
+    if (a->heads < 1 || a->heads > 65535 || a->heads % c.H)
+        return fail(SPFFN_E_SHAPE, "attn_step: heads=%d is no multiple of kv_heads=%d", a->heads,
+                    c.H);
+    if (max_new < 1 || max_new > 64)
+        return fail(SPFFN_E_SHAPE, "attn_step: max_new=%d outside [1, 64]", max_new);
+    const int64_t row = (int64_t)a->heads * c.D;
+    w.n_qkv = row + 2 * (int64_t)c.H * c.D;
+    if (a->qkv.rows != w.n_qkv || a->out.cols != row || a->out.rows != a->qkv.cols)
+        return fail(SPFFN_E_SHAPE,
+                    "attn_step: qkv is [%d, %d] and out [%d, %d], %d and %d heads of %d need "
+                    "[%lld, d] and [d, %lld]",
+                    a->qkv.rows, a->qkv.cols, a->out.rows, a->out.cols, a->heads, c.H, c.D,
+                    (long long)w.n_qkv, (long long)row);
+    for (const spffn_q4_matrix *m : {&a->qkv, &a->out})
+        if (!q4_sizes_ok(m->rows, m->cols, m->group))
+            return fail(SPFFN_E_SHAPE, "attn_step: a matrix [%d, %d] in groups of %d", m->rows, m->cols,
+                        m->group);
+    size_t call = attn_ws_bytes(a->heads, c.H, c.D, max_new, false);
+    const size_t m1 = q4_ws_bytes(a->qkv.rows, a->qkv.cols, B);
+    const size_t m2 = q4_ws_bytes(a->out.rows, a->out.cols, B);
+    call = call > m1 ? call : m1;
+    call = call > m2 ? call : m2;
+    w.qkv = 0;
+    w.att = up256((size_t)B * w.n_qkv * 4);
+    w.call = w.att + up256((size_t)B * row * 4);
+    w.total = w.call + up256(call);
+    return SPFFN_OK;
+}
+
+}  // namespace
+
+size_t spffn_attn_workspace_bytes(const spffn_attn_desc *attn, const spffn_kv_cache *cache,
+                                  int32_t B, int32_t max_new) {
+    KvCache c;
+    AttnWs w;
+    return attn_sizes(attn, cache, B, max_new, c, w) == SPFFN_OK ? w.total : 0;
+}
+
+spffn_status spffn_attn_step(const spffn_attn_desc *attn, const spffn_kv_cache *cache,
+                             const float *x, float *h, int32_t B, const int32_t *slots,
+                             const int32_t *starts, const int32_t *lens, const int32_t *table,
+                             int32_t R, int32_t width, const int64_t *mask, int32_t max_new,
+                             void *ws, size_t ws_bytes, void *stream) {
+    KvCache c;
+    AttnWs w;
+    if (spffn_status st = attn_sizes(attn, cache, B, max_new, c, w)) return st;
+    if (!x || !h || !aligned(x, 16) || !aligned(h, 16))
+        return fail(SPFFN_E_ARG, "attn_step: x and h must be 16-byte aligned and not NULL");
+    const size_t nx = (size_t)B * attn->qkv.cols * 4;
+    if (x != h && overlap(x, nx, h, nx))
+        return fail(SPFFN_E_ARG, "attn_step: h overlaps part of x");
+    if (!(attn->rms_eps >= 0.0f) || std::isinf(attn->rms_eps))
+        return fail(SPFFN_E_ARG, "attn_step: rms_eps must be finite and >= 0");
+    // all of the calls' arguments are checked before the first launch
+    if (!slots || !aligned(slots, 4))
+        return fail(SPFFN_E_ARG, "attn_step: NULL or misaligned slots");
+    if (spffn_status st = check_ws(w.total, ws, ws_bytes)) return st;
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    float *qkv = reinterpret_cast<float *>(base + w.qkv), *att = reinterpret_cast<float *>(base + w.att);
+    void *call = base + w.call;
+    const size_t nb = ws_bytes - w.call;
+    const int64_t row = (int64_t)attn->heads * c.D;
+    // with no tokens it only checks its sizes, before anything is launched
+    const auto attention = [&](int32_t n) {
+        return attend("attn_step", true, cache, qkv, SPFFN_F32, w.n_qkv, n, attn->heads, starts, lens,
+                      table, R, width, mask, max_new, attn->scale, att, row, call, nb, stream);
+    };
+    if (!starts || !lens || !table || !aligned(starts, 4) || !aligned(lens, 4) ||
+        !aligned(table, 4) || !aligned(mask, 8))
+        return fail(SPFFN_E_ARG, "attn_step: NULL or misaligned starts, lens, table or mask");
+    if (spffn_status st = attention(0)) return st;
+    if (!attn->qkv.packed || !attn->out.packed || !aligned(attn->qkv.packed, 16) ||
+        !aligned(attn->out.packed, 16) || !aligned(attn->qkv_bias, 4) || !aligned(attn->out_bias, 4))
+        return fail(SPFFN_E_ARG, "attn_step: NULL or misaligned matrix, or misaligned bias");
+    if (spffn_status st = spffn_q4_matvec(&attn->qkv, x, B, attn->rms_eps, attn->qkv_bias, nullptr,
+                                          qkv, call, nb, stream))
+        return st;
+    if (spffn_status st = spffn_kv_append(cache, qkv + row, qkv + row + (int64_t)c.H * c.D, SPFFN_F32,
+                                          w.n_qkv, w.n_qkv, slots, B, stream))
+        return st;
+    if (spffn_status st = attention(B)) return st;
+    return spffn_q4_matvec(&attn->out, att, B, -1.0f, attn->out_bias, x, h, call, nb, stream);
 }
 
 spffn_status spffn_stream_read(const void *buf, int64_t bytes, uint32_t *sink, void *stream) {

@@ -89,6 +89,7 @@ struct Args {
     int N, R, G, H, width, pages, shift, max_new;
     int narrow;  // R <= 64 and every position fits 31 bits
     int wq;  // waves along the columns (1, 2, 4); 4 / wq along the tokens
+    bool clear;  // the join kernel writes zeros to the rows that no request names
 };
 
 // What a request asks for: committed length L, tokens T, keys tot = L + T.
@@ -886,6 +887,22 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(Args a, int wgs, 
     __shared__ uint16_t list[kMaxWgs];
     __shared__ int count[kMaxWgs / 64];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    // ---- rows without a request, by the workgroups that get no task first ----
+    if (a.clear)
+        for (int row = gridDim.x - 1 - blockIdx.x; row < a.N; row += gridDim.x) {
+            bool named = false;
+            for (int r = threadIdx.x; r < a.R; r += kThreads) {
+                const int from = max(a.starts[r], 0), to = min(a.starts[r + 1], a.N);
+                named |= row >= from && row < to && row - from < a.max_new;
+            }
+            if (__syncthreads_or(named)) continue;
+            for (int64_t i = threadIdx.x; i < (int64_t)a.H * a.G * D; i += kThreads) {
+                if constexpr (Q16)
+                    static_cast<_Float16 *>(a.out)[row * a.ldo + i] = (_Float16)0.0f;
+                else
+                    static_cast<float *>(a.out)[row * a.ldo + i] = 0.0f;
+            }
+        }
     // ---- the tasks, in order ----
     uint64_t have[kMaxWgs / kThreads];
 #pragma unroll

@@ -209,6 +209,7 @@ struct AttnCall {
     int R, width, max_new;
     const int64_t *mask;
     float scale;
+    bool clear;  // rows that no request names become zeros (else they stay as they are)
 };
 size_t attn_ws_bytes(int heads, int kv_heads, int dim, int max_new, bool q16);
 hipError_t launch_tree_attention(const KvCache &c, const AttnCall &q, void *ws, hipStream_t s);

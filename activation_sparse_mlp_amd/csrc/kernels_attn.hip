@@ -67,6 +67,7 @@ hipError_t launch_tree_attention(const KvCache &c, const AttnCall &q, void *ws, 
     const int64_t groups = ((int64_t)q.max_new * G + sh.cols - 1) / sh.cols;
     a.narrow = q.R <= 64 && steps * groups * c.H * q.R < (int64_t)1 << 31;
     a.wq = sh.wq;
+    a.clear = q.clear;
     return c.fp8 ? launch_attend_fp8(a, q.q16, c.D, sh.mode, s)
                  : launch_attend_f16(a, q.q16, c.D, sh.mode, s);
 }

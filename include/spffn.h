@@ -455,6 +455,36 @@ spffn_status spffn_tree_attention(const spffn_kv_cache *cache, const void *q, in
                                   void *out, int64_t ld_out, void *ws, size_t ws_bytes,
                                   void *stream);
 
+/* [host] The attention of one layer: W_qkv [(heads + 2 kv_heads) * head_dim, d]
+ * (queries, then keys, then values), W_out [d, heads * head_dim], biases fp32 of
+ * their rows or NULL, the epsilon of the RMS norm and the factor of the scores. */
+typedef struct {
+    spffn_q4_matrix qkv, out;
+    const float *qkv_bias, *out_bias;
+    int32_t heads;
+    float rms_eps, scale;
+} spffn_attn_desc;
+
+/* The attention half of one layer for B <= SPFFN_MAX_BATCH tokens, all on
+ * `stream`, to be followed by the layer's FFN (spffn_decode_step of a one-layer
+ * model) on the same residual stream:
+ *   n_b = x_b / sqrt(mean(x_b^2) + rms_eps)             (gainless RMS norm)
+ *   q, k, v = W_qkv n_b + bias;  k, v go to slots[b] of the cache
+ *   h_b = x_b + W_out attention(q) + bias
+ * starts, lens, table, mask, max_new: as spffn_tree_attention (N = B); slots: as
+ * spffn_kv_append.  spffn_block_tables makes starts and slots, once per step for
+ * every layer.  The attention of a token that no request names is zero (a padded
+ * batch's rows: h_b = x_b + bias).  No position is encoded here (learned embeddings come with x).
+ * x == h updates in place.  kv_heads and head_dim are the cache's.  ws:
+ * spffn_attn_workspace_bytes bytes, 256-byte aligned. */
+size_t spffn_attn_workspace_bytes(const spffn_attn_desc *attn, const spffn_kv_cache *cache,
+                                  int32_t B, int32_t max_new);
+spffn_status spffn_attn_step(const spffn_attn_desc *attn, const spffn_kv_cache *cache,
+                             const float *x, float *h, int32_t B, const int32_t *slots,
+                             const int32_t *starts, const int32_t *lens, const int32_t *table,
+                             int32_t R, int32_t width, const int64_t *mask, int32_t max_new,
+                             void *ws, size_t ws_bytes, void *stream);
+
 /* ---- load-time utilities ---------------------------------------------- */
 
 /* Activation profile over N tokens x [N, d] (N >= 1): counts[i] (device

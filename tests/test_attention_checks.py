@@ -191,6 +191,36 @@ def test_workspace_bytes():
         assert nb(ref, heads, new, dtype) == 0
 
 
+def attn_step(**kw):
+    from activation_sparse_mlp_amd._lib import AttnDesc
+    a = dict(rows=(4 + 2 * 2) * 64, cols=96, out_rows=96, out_cols=256, heads=4, eps=1e-5, scale=0.1,
+             qkv_packed=at(2), out_packed=at(3), qkv_bias=None, x=at(4), h=at(5), B=3, slots=at(6),
+             starts=at(7), lens=at(8), table=at(9), R=2, width=5, mask=None, max_new=3, ws=at(10),
+             nb=1 << 27)
+    a.update(kw)
+    d = AttnDesc(qkv=q4(packed=a["qkv_packed"], rows=a["rows"], cols=a["cols"]),
+                 out=q4(packed=a["out_packed"], rows=a["out_rows"], cols=a["out_cols"]),
+                 qkv_bias=a["qkv_bias"], heads=a["heads"], rms_eps=a["eps"], scale=a["scale"])
+    return spffn.load().spffn_attn_step(
+        C.byref(d), C.byref(cache()), a["x"], a["h"], a["B"], a["slots"], a["starts"], a["lens"],
+        a["table"], a["R"], a["width"], a["mask"], a["max_new"], a["ws"], a["nb"], None)
+
+
+@pytest.mark.parametrize("status,kw", [
+    *[(E_ARG, {k: None}) for k in ("x", "h", "slots", "starts", "lens", "table", "qkv_packed",
+                                   "out_packed")],
+    (E_ARG, dict(h=at(4) + 64)), (E_ARG, dict(x=at(4) + 4)), (E_ARG, dict(eps=-1.0)),
+    (E_ARG, dict(scale=float("nan"))), (E_ARG, dict(qkv_bias=at(1) + 2)),
+    (E_SHAPE, dict(B=0)), (E_SHAPE, dict(B=17)), (E_SHAPE, dict(heads=3)),
+    (E_SHAPE, dict(rows=512 + 16)), (E_SHAPE, dict(out_cols=288)), (E_SHAPE, dict(out_rows=128)),
+    (E_SHAPE, dict(max_new=65)), (E_SHAPE, dict(R=0)), (E_SHAPE, dict(width=0)),
+    (E_WORKSPACE, dict(ws=None)), (E_WORKSPACE, dict(nb=4096)),
+])
+def test_attn_step(status, kw):
+    assert attn_step(**kw) == status
+    assert spffn.load().spffn_last_error()
+
+
 # --------------------------------------------------------------------------- binding
 def _u8(*s):
     return torch.zeros(*s, dtype=torch.uint8)
