@@ -386,7 +386,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppArgs a) {
 
 template <int D, int T>
 hipError_t launch_append_dim(const KvCache &c, const AppArgs &a, bool src16, hipStream_t s) {
-    const dim3 grid((a.N + T - 1) / T, c.H, 2);
+    const dim3 grid((a.N - 1) / T + 1, c.H, 2);
     if (c.fp8) {
         if (src16) kv_append_kernel<true, true, D, T><<<grid, 256, 0, s>>>(a);
         else kv_append_kernel<true, false, D, T><<<grid, 256, 0, s>>>(a);

@@ -17,17 +17,27 @@
 //     product of a subnormal drops low bits.)  The scale is applied in fp32 to a
 //     group's sum, so no weight is ever rounded;
 //   * activations are the B operand, hi + lo halves of x scaled by a power of
-//     two per token and block of 128 columns (largest magnitude in [2^14,
-//     2^15)): about 22 significant bits down to 2^-18 of the block's largest,
-//     an absolute 2^-40 of it below.  For B <= 8 the hi halves are columns 0..7
-//     and the lo halves columns 8..15 of one instruction, for B > 8 they take one
-//     each into the same accumulator;
-//   * a wave owns whole blocks of 128 columns (wave, wave + W, ...) of RT tiles
-//     of 16 rows, so it splits each activation once and no wave waits for
-//     another before the final sum over the workgroup's waves, which is taken
-//     in a fixed order.  The RMS scale needs no pass of its own: it has no gain,
-//     so it is one factor per token at the end, and each wave already holds the
-//     activations whose squares it sums.
+//     two (largest magnitude in [2^14, 2^15)): about 22 significant bits down to
+//     2^-18 of the largest, an absolute 2^-40 of it below.  For B <= 8 the hi
+//     halves are columns 0..7 and the lo halves columns 8..15 of one instruction,
+//     for B > 8 they take one each into the same accumulator;
+//   * B <= 2 is one launch: a wave owns whole blocks of 128 columns (wave, wave +
+//     W, ...) of a tile of 16 rows and splits their activations itself, with a
+//     scale per token and block; no wave waits for another before the final sum,
+//     which is taken in a fixed order;
+//   * B > 2 splits the activations in a launch of its own, and the product reads
+//     the halves from L2.  (Sharing them through LDS between waves of different
+//     rows, a barrier every two or four blocks, was slower: 9216 x 8192 and five
+//     tokens 22.9 us against 20.3, 36864 x 12288 and sixteen 78.7 against 72.)
+//     The RMS norm needs no pass of its own in either: it has no gain, so it is
+//     one factor per token at the end.
+//
+// Measured in a replayed graph: 4096 x 4096, one token 5.4 us (9.5 MB, mostly the
+// launch and one chain of loads); 10240 x 8192, one token 16.6 us (44 MB, 2.65
+// TB/s); 9216 x 8192, five tokens 20.3 us; 36864 x 12288, sixteen tokens 72 to 77
+// us (244 MB, 3.3 TB/s).  A plain read of as many bytes reaches 7 TB/s: between
+// the two stand the waits of each wave for its own codes, since a block's work is
+// short (a deeper prefetch costs more waves than it saves).
 //
 // Packed layout (launch_q4_pack): per tile of 16 rows and block of 128 columns
 // 1 KiB of codes in the order of one wave's 16-byte loads -- lane l = 16 g + m

@@ -358,9 +358,9 @@ spffn_status spffn_q4_pack(const uint8_t *codes, const void *scales, const uint8
  * applies before a layer; rms_eps < 0: r_b = 1.  Weights are exact (the scale
  * is applied to a group's sum), sums are fp32 in a fixed order.  A token whose
  * activations are not all finite gets NaN or infinities, the others are as
- * without it.  y must not overlap x.  ws: spffn_q4_matvec_workspace_bytes bytes, 256-byte aligned (none,
- * and ws ignored, for B <= 2; 0 on bad input too); it holds nothing between
- * calls, and calls that overlap need one each. */
+ * without it.  y must not overlap x.  ws: spffn_q4_matvec_workspace_bytes
+ * bytes, 256-byte aligned (none, and ws ignored, for B <= 2; 0 on bad input
+ * too); it holds nothing between calls, and calls that overlap need one each. */
 size_t spffn_q4_matvec_workspace_bytes(const spffn_q4_matrix *w, int32_t B);
 spffn_status spffn_q4_matvec(const spffn_q4_matrix *w, const float *x, int32_t B, float rms_eps,
                              const float *bias, const float *resid, float *y, void *ws,
@@ -473,10 +473,12 @@ typedef struct {
  *   h_b = x_b + W_out attention(q) + bias
  * starts, lens, table, mask, max_new: as spffn_tree_attention (N = B); slots: as
  * spffn_kv_append.  spffn_block_tables makes starts and slots, once per step for
- * every layer.  The attention of a token that no request names is zero (a padded
- * batch's rows: h_b = x_b + bias).  No position is encoded here (learned embeddings come with x).
- * x == h updates in place.  kv_heads and head_dim are the cache's.  ws:
- * spffn_attn_workspace_bytes bytes, 256-byte aligned. */
+ * every layer.  The attention of a token that no request names, or behind the
+ * first max_new of its request, is zero (a padded batch's rows: h_b = x_b +
+ * bias).  No position is encoded here (learned embeddings come with x).  x and h
+ * are 16-byte aligned; x == h updates in place.  kv_heads and head_dim are the
+ * cache's, and slots names a row at most once.  ws: spffn_attn_workspace_bytes bytes, 256-byte aligned; calls
+ * that may overlap need one each. */
 size_t spffn_attn_workspace_bytes(const spffn_attn_desc *attn, const spffn_kv_cache *cache,
                                   int32_t B, int32_t max_new);
 spffn_status spffn_attn_step(const spffn_attn_desc *attn, const spffn_kv_cache *cache,
