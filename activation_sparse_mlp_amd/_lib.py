@@ -623,11 +623,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _call(index, name, *args):
     """One entry point on the current stream of GPU `index`, which need not be
     the current device."""
     fn = getattr(_lib or load(), name)
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:  # (tensors on a GPU: it is initialised)
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -752,18 +755,18 @@ def block_tables(lens, adds, table, free_list, n_free, page_size, n_tokens, star
     [1].  Returns dict(starts [R + 1], new_lens [R], slots [n_tokens], positions
     [n_tokens], left [2] = free pages left and requests not served); slots and
     positions are -1 from starts[R] on, slots also for requests not served."""
-    R = lens.numel()
-    if table.dim() != 2 or table.shape[0] != R:
-        raise ValueError(f"table must have shape [{R}, width], got {tuple(table.shape)}")
-    n, i32, width = int(n_tokens), torch.int32, table.shape[1]
+    R, shape = lens.numel(), table.shape
+    if len(shape) != 2 or shape[0] != R:
+        raise ValueError(f"table must have shape [{R}, width], got {tuple(shape)}")
+    n, i32, width = int(n_tokens), torch.int32, shape[1]
     if n < 0:
         raise ValueError(f"n_tokens={n_tokens} < 0")
     _sizes((adds, R, "adds"), (n_free, 1, "n_free"), (starts, R + 1, "starts"),
            (new_lens, R, "new_lens"), (slots, n, "slots"), (positions, n, "positions"),
            (left, 2, "left"))
     _dev(lens, i32, "lens")
-    dev, index, cap = lens.device, lens.get_device(), free_list.numel()
-    new = lambda k: torch.empty(k, dtype=i32, device=dev)  # noqa: E731
+    index, cap = lens.get_device(), free_list.numel()
+    new = lambda k: torch.empty(k, dtype=i32, device=lens.device)  # noqa: E731
     starts = new(R + 1) if starts is None else starts
     new_lens = new(R) if new_lens is None else new_lens
     slots = new(n) if slots is None else slots
