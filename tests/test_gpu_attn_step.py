@@ -196,3 +196,47 @@ def test_tokens_of_no_request_get_the_bias_alone():
         # 0 W + bias + x, in either order of one fp32 addition
         assert torch.equal(h[rest], (x + bias)[rest])
         assert not torch.equal(h[1], (x + bias)[1])
+
+
+def test_two_streams_at_once():
+    # calls that overlap take a workspace each; what they compute is what they do alone
+    stacks = [Stack(1, torch.float16, seed=15 + i) for i in range(2)]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    x = torch.randn(6, stacks[0].d, device=DEV)
+    args = (i32([0, 6]), i32([10]), i32(range(26, 32)), i32([[1]]))
+    want = [spffn.attn_step(s.attn[0], s.cache[0][0], x, *args).clone() for s in stacks]
+    streams, got = [torch.cuda.Stream() for _ in stacks], [None, None]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, (s, stream) in enumerate(zip(stacks, streams)):
+            with torch.cuda.stream(stream):
+                got[i] = spffn.attn_step(s.attn[0], s.cache[0][0], x, *args)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_two_graphs_share_a_workspace():
+    s = Stack(1, torch.float8_e4m3fn, seed=17)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    ws = s.attn[0].workspace(s.cache[0][0], 16, 8)
+    runs = []
+    for B in (5, 16):  # the two shapes of the product
+        x = torch.randn(B, s.d, device=DEV)
+        h = torch.empty_like(x)
+        args = (i32([0, min(B, 8)]), i32([20]), i32([-1] * B), i32([[2, 5]]))
+        call = lambda x=x, h=h, args=args: spffn.attn_step(  # noqa: E731
+            s.attn[0], s.cache[0][0], x, *args, max_new=8, h=h, ws=ws)
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        runs.append((x, h, call, graph))
+    for i in range(3):
+        for x, h, call, graph in runs:
+            x.copy_(torch.randn(x.shape))
+            want = call().clone()
+            h.zero_()
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(h, want), (i, x.shape[0])

@@ -153,3 +153,17 @@ def test_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want), i
+
+
+@pytest.mark.parametrize("B", [1, 2, 7, 16])
+def test_views_that_are_only_aligned_to_an_element(B):
+    rows, cols = 77, 416
+    w, host, g = make(rows, cols, 32, True, seed=8)
+    x = torch.randn(B, cols, generator=g)
+    bias, resid = torch.randn(rows, generator=g), torch.randn(B, rows, generator=g)
+    at = lambda t: torch.cat([t.new_zeros(1), t.flatten()]).to(DEV)[1:].view(t.shape)  # noqa: E731
+    y = at(torch.zeros(B, rows))
+    got = spffn.q4_matvec(w, x.to(DEV), bias=at(bias), resid=at(resid), y=y)
+    want, bound = ref.q4_matvec(host, x, bias, resid)
+    assert got is y
+    ref.close(got.cpu(), want, bound)
