@@ -865,6 +865,12 @@ spffn_status check_cache(const char *who, const spffn_kv_cache *c, KvCache &out)
     return SPFFN_OK;
 }
 
+// Whether [p, p + n) shares bytes with the cache's pages.
+bool in_cache(const KvCache &c, const void *p, size_t n) {
+    const size_t bytes = ((size_t)c.pages << c.shift) * c.H * c.D * (c.fp8 ? 1 : 2);
+    return overlap(p, n, c.k, bytes) || overlap(p, n, c.v, bytes);
+}
+
 // A strided activation [N, row] of fp32 or fp16 elements.
 spffn_status check_rows(const char *who, const char *name, const void *p, int32_t dtype, int64_t ld,
                         int64_t row) {
@@ -929,8 +935,11 @@ spffn_status spffn_q4_matvec(const spffn_q4_matrix *w, const float *x, int32_t B
     if ((resid && resid != y && overlap(y, ny, resid, ny)) ||
         (bias && overlap(y, ny, bias, (size_t)w->rows * 4)))
         return fail(SPFFN_E_ARG, "q4_matvec: y overlaps bias or part of resid");
-    if (const size_t need = q4_ws_bytes(w->rows, w->cols, B))
+    if (const size_t need = q4_ws_bytes(w->rows, w->cols, B)) {
         if (spffn_status st = check_ws(need, ws, ws_bytes)) return st;
+        if (overlap(ws, need, x, (size_t)B * w->cols * 4) || overlap(ws, need, y, ny))
+            return fail(SPFFN_E_ARG, "q4_matvec: the workspace overlaps x or y");
+    }
     SPFFN_HIP(launch_q4_matvec(static_cast<const uint8_t *>(w->packed), w->rows, w->cols, w->group,
                                w->zeros != 0, x, B, rms_eps, bias, resid, y, ws,
                                (hipStream_t)stream),
@@ -990,6 +999,10 @@ spffn_status spffn_kv_append(const spffn_kv_cache *cache, const void *k, const v
     if (spffn_status st = check_rows("kv_append", "v", v, dtype, ld_v, row)) return st;
     if (!slots || !aligned(slots, 4))
         return fail(SPFFN_E_ARG, "kv_append: NULL or misaligned slots");
+    const int es = dtype == SPFFN_F16 ? 2 : 4;
+    if (in_cache(c, k, ((size_t)(N - 1) * ld_k + row) * es) ||
+        in_cache(c, v, ((size_t)(N - 1) * ld_v + row) * es) || in_cache(c, slots, (size_t)N * 4))
+        return fail(SPFFN_E_ARG, "kv_append: k, v or slots overlap the cache");
     SPFFN_HIP(launch_kv_append(c, k, v, dtype == SPFFN_F16, ld_k, ld_v, slots, N,
                                (hipStream_t)stream),
               "cache append launch");
@@ -1039,11 +1052,16 @@ spffn_status attend(const char *who, bool clear, const spffn_kv_cache *cache, co
     const int es = dtype == SPFFN_F16 ? 2 : 4;
     if (overlap(q, ((size_t)(N - 1) * ld_q + row) * es, out, ((size_t)(N - 1) * ld_out + row) * es))
         return fail(SPFFN_E_ARG, "%s: q and out overlap", who);
+    if (in_cache(c, out, ((size_t)(N - 1) * ld_out + row) * es))
+        return fail(SPFFN_E_ARG, "%s: out overlaps the cache", who);
     if (!starts || !lens || !table || !aligned(starts, 4) || !aligned(lens, 4) ||
         !aligned(table, 4) || !aligned(mask, 8))
         return fail(SPFFN_E_ARG, "%s: NULL or misaligned starts, lens, table or mask", who);
     const size_t need = attn_ws_bytes(heads, c.H, c.D, max_new, dtype == SPFFN_F16);
     if (spffn_status st = check_ws(need, ws, ws_bytes)) return st;
+    if (overlap(ws, need, out, ((size_t)(N - 1) * ld_out + row) * es) ||
+        overlap(ws, need, q, ((size_t)(N - 1) * ld_q + row) * es) || in_cache(c, ws, need))
+        return fail(SPFFN_E_ARG, "%s: the workspace overlaps q, out or the cache", who);
     AttnCall a{q, out, dtype == SPFFN_F16, ld_q, ld_out, N, heads, starts, lens, table,
                R, width, max_new, mask, scale, clear};
     SPFFN_HIP(launch_tree_attention(c, a, ws, (hipStream_t)stream), "attention launch");
@@ -1133,6 +1151,9 @@ spffn_status spffn_attn_step(const spffn_attn_desc *attn, const spffn_kv_cache *
     if (!slots || !aligned(slots, 4))
         return fail(SPFFN_E_ARG, "attn_step: NULL or misaligned slots");
     if (spffn_status st = check_ws(w.total, ws, ws_bytes)) return st;
+    if (overlap(ws, w.total, x, nx) || overlap(ws, w.total, h, nx) || in_cache(c, ws, w.total) ||
+        in_cache(c, h, nx))
+        return fail(SPFFN_E_ARG, "attn_step: the workspace overlaps x or h, or the cache one of them");
     uint8_t *base = static_cast<uint8_t *>(ws);
     float *qkv = reinterpret_cast<float *>(base + w.qkv), *att = reinterpret_cast<float *>(base + w.att);
     void *call = base + w.call;

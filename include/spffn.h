@@ -358,9 +358,10 @@ spffn_status spffn_q4_pack(const uint8_t *codes, const void *scales, const uint8
  * applies before a layer; rms_eps < 0: r_b = 1.  Weights are exact (the scale
  * is applied to a group's sum), sums are fp32 in a fixed order.  A token whose
  * activations are not all finite gets NaN or infinities, the others are as
- * without it.  y must not overlap x.  ws: spffn_q4_matvec_workspace_bytes
- * bytes, 256-byte aligned (none, and ws ignored, for B <= 2; 0 on bad input
- * too); it holds nothing between calls, and calls that overlap need one each. */
+ * without it.  y and ws must not overlap x or each other.  ws:
+ * spffn_q4_matvec_workspace_bytes bytes, 256-byte aligned (none, and ws ignored,
+ * for B <= 2; 0 on bad input too); it holds nothing between calls, and calls that
+ * overlap need one each. */
 size_t spffn_q4_matvec_workspace_bytes(const spffn_q4_matrix *w, int32_t B);
 spffn_status spffn_q4_matvec(const spffn_q4_matrix *w, const float *x, int32_t B, float rms_eps,
                              const float *bias, const float *resid, float *y, void *ws,
@@ -418,7 +419,8 @@ typedef struct {
  * a wider projection are fine); rows 16-byte aligned.  Elements are rounded
  * once: fp16 to nearest, fp8 the nearest E4M3 value of x / scale, saturating at
  * +-448.  Rows of the cache that no slot names keep their bits.  A slot given
- * twice ends with elements of either row. */
+ * twice ends with elements of either row.  The inputs must not overlap the
+ * cache. */
 spffn_status spffn_kv_append(const spffn_kv_cache *cache, const void *k, const void *v,
                              int32_t dtype, int64_t ld_k, int64_t ld_v, const int32_t *slots,
                              int32_t N, void *stream);
@@ -428,7 +430,7 @@ spffn_status spffn_kv_append(const spffn_kv_cache *cache, const void *k, const v
  *   q, out [N, heads, head_dim]  SPFFN_F32 or SPFFN_F16 (dtype, both the same),
  *              token n at q + n * ld_q elements, rows 16-byte aligned; heads a
  *              multiple of kv_heads (query head i reads kv head i / (heads /
- *              kv_heads)); q and out must not overlap
+ *              kv_heads)); q, out, the cache and ws must not overlap
  *   starts int32 [R + 1]  request r's tokens are starts[r] .. starts[r + 1]
  *   lens int32 [R]     tokens of r in the cache before this step
  *   table int32 [R, width]  its pages

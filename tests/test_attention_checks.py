@@ -314,3 +314,19 @@ def test_rows_and_counts():
         spffn.kv_append(FakeCache, torch.zeros(3, 2, 32), torch.zeros(3, 2, 64), _i(3))
     with pytest.raises(TypeError, match="CUDA"):
         spffn.kv_append(FakeCache, torch.zeros(3, 2, 64), torch.zeros(3, 2, 64), _i(3))
+
+
+# --------------------------------------------------------------------------- memory that overlaps
+@pytest.mark.parametrize("call", [
+    lambda c: append(c, k=c.k + 256), lambda c: append(c, v=c.v), lambda c: append(c, k=c.v),
+    lambda c: append(c, k=c.k - 128 * 4 * 2),              # the last row of three
+    lambda c: append(c, slots=c.k + 16),
+    lambda c: attend(c, out=c.v + 512), lambda c: attend(c, out=c.k),
+    lambda c: attend(c, ws=at(9)), lambda c: attend(c, ws=at(4)), lambda c: attend(c, ws=c.k),
+    lambda c: matvec(B=5, ws=at(1)), lambda c: matvec(B=5, ws=at(2)),
+    lambda c: attn_step(ws=at(4)), lambda c: attn_step(ws=at(5)), lambda c: attn_step(ws=c.v),
+    lambda c: attn_step(x=c.k, h=c.k),
+])
+def test_overlaps(call):
+    assert call(cache()) == E_ARG
+    assert "overlap" in spffn.load().spffn_last_error().decode()
